@@ -426,6 +426,132 @@ int thd_sparse_mla_fwd(const void* q, const void* kv, const int32_t* indices,
 /* Synchronises the stream; returns and clears the sparse-MLA status word. */
 int thd_sparse_mla_get_error(void* stream);
 
+/*
+ * ------------------------------------------------------- serving: paged cache
+ * One step of a batch of requests that continue the same prompt: the prompt's
+ * keys and values are in the cache once, in the pages of `prefix_table`, and
+ * every request has pages of its own for its further tokens.  A page (block)
+ * holds block_size tokens; slot = block * block_size + token of the block.
+ * The pages print no serving path: the three entry points below carry the
+ * packed-THD attention ("muse_spark.magi_cp" and "flint.magi" pages: causal or
+ * sliding-window, GQA, sinks) from the prompt to the answer.  Lengths and
+ * tables are DEVICE arrays, so that a captured CUDA graph follows them; none
+ * of the three allocates device memory, so all three can be captured.
+ *
+ * thd_kv_block_tables: the step's pages, block tables, slots and positions
+ * from the request lengths.  Request b, with n = seq_lens[b] cached tokens and
+ * m = new_lens[b]:
+ *   n < 0           a vacant entry: nothing happens, seq_lens_out[b] = -1
+ *   n >= 0, m < 0   the request ends: its ceil(n / block_size) pages go back
+ *                   onto the stack of free pages, seq_lens_out[b] = -1
+ *   n >= 0, m >= 0  it gets pages until they hold n + m tokens, appended to
+ *                   its row of block_tables, seq_lens_out[b] = n + m
+ * Free pages are a stack: free_blocks[0 .. *free_count), its last entry on
+ * top.  First the pages of ended requests are pushed (in request order, then
+ * table order), then the growing requests pop theirs in request order.  A
+ * request with m > 0 is refused -- no page, no slot, seq_lens_out[b] = n --
+ * when n + m tokens do not fit max_blocks pages, when its rows do not fit
+ * n_rows, or when the pages wanted by it and the growing requests before it
+ * (refused for want of pages or not) are more than there are and it wants any.
+ *   seq_lens, new_lens  int32 [n_req]
+ *   block_tables        int32 [n_req, max_blocks], dense; only new entries are
+ *                       written
+ *   free_blocks         int32 [free_capacity]; only pushed entries are written
+ *   free_count          int32 [1], free_count_out int32 [1] (may be the same)
+ *   first_position_or_null  int32 [1] added to every position (the length of
+ *                       a shared prefix), NULL = 0
+ *   seq_lens_out        int32 [n_req], may be seq_lens
+ *   cu_new              int32 [n_req + 1]: the packed rows of the requests
+ *                       (exclusive sums of their m, refused ones included;
+ *                       at most 2^31 - 1)
+ *   slots, positions    int32 [n_rows]: cache slot (-1 for rows of refused
+ *                       requests and behind the last row) and position (0
+ *                       behind the last row) of every packed row
+ *   refused             int32 [1]: how many requests were refused
+ * 1 <= n_req <= 8192 (else THD_ERR_UNSUPPORTED), n_rows >= 0, block_size >= 1,
+ * max_blocks >= 1, free_capacity >= 0; all pointers 4-byte aligned.
+ * n_req = 0 is a no-op.  Deterministic (no atomics).  One launch.
+ */
+int thd_kv_block_tables(const int32_t* seq_lens, const int32_t* new_lens, int n_req, int block_size,
+                        int32_t* block_tables, int max_blocks,
+                        int32_t* free_blocks, int64_t free_capacity, const int32_t* free_count,
+                        const int32_t* first_position_or_null, int64_t n_rows,
+                        int32_t* seq_lens_out, int32_t* free_count_out, int32_t* cu_new,
+                        int32_t* slots, int32_t* positions, int32_t* refused, void* stream);
+
+/*
+ * Writes key and value rows into a paged cache: for every row r with
+ * 0 <= slots[r] < num_blocks * block_size, k_cache[slots[r]] = k[r] and
+ * v_cache[slots[r]] = v[r]; other rows are skipped.  Slots inside the range
+ * have to be distinct (those of thd_kv_block_tables are); a slot given twice
+ * holds a mixture of the rows.
+ *   k, v           bf16 device [n_rows, Hkv, D], rows k_row_stride /
+ *                  v_row_stride elements apart (so they may lie inside the
+ *                  output of a fused projection), heads dense
+ *   slots          int32 device [n_rows]
+ *   k_cache, v_cache  bf16 device [num_blocks, block_size, Hkv, D] with D
+ *                  dense and the element strides block_stride, token_stride,
+ *                  head_stride (the same for both), so heads may also be the
+ *                  outer dimension of a block and the two caches may be
+ *                  interleaved
+ * D 64, 128 or 256 (else THD_ERR_UNSUPPORTED); 16-byte aligned pointers and
+ * strides (multiples of 8 elements); num_blocks * block_size < 2^31.
+ */
+int thd_kv_write(const void* k, const void* v, int64_t k_row_stride, int64_t v_row_stride,
+                 const int32_t* slots, int64_t n_rows, int Hkv, int D,
+                 void* k_cache, void* v_cache, int64_t num_blocks, int block_size,
+                 int64_t block_stride, int64_t token_stride, int64_t head_stride, void* stream);
+
+/*
+ * Attention of a step's new tokens over the shared prefix, computed once for
+ * the whole batch, and over each request's own pages.  Request b has the
+ * sequence of the P = *prefix_len prefix tokens followed by its n = kv_lens[b]
+ * own ones, whose keys and values are all in the cache; its n_q queries are
+ * the last n_q tokens of that sequence.  Query i is at position
+ * p = P + n - n_q + i and sees the keys max(0, p - window + 1) <= j <= p
+ * (window 0: 0 <= j <= p) with the scores, sinks, output and log-sum-exp of
+ * thd_attn_fwd.  Without a prefix this is decoding from the paged cache.
+ *   q              bf16 [n_req * n_q, Hq, D] (request-major)
+ *   k_cache, v_cache and strides  as thd_kv_write
+ *   prefix_table_or_null  int32 [prefix_blocks], NULL exactly when
+ *                  prefix_len_or_null is (no prefix)
+ *   prefix_len_or_null    int32 [1]
+ *   block_tables   int32 [n_req, max_blocks], rows dense
+ *   kv_lens        int32 [n_req]; n < 0 marks a vacant entry, whose rows of
+ *                  out and lse are left as they are
+ *   out            bf16 [n_req * n_q, Hq, D]
+ *   lse            fp32 [n_req * n_q, Hq] or NULL
+ *   workspace      device scratch of at least
+ *                  thd_attn_shared_prefix_workspace_bytes(...), 16-byte
+ *                  aligned; its contents on entry do not matter.  Calls that
+ *                  may run at the same time need one each.
+ * A length beyond its table is cut to what the table holds.  A table entry
+ * outside [0, num_blocks) contributes no keys.  A row that sees no key gets
+ * out = 0 and lse = -inf (with sinks: the sink logit).  Cache contents that no
+ * query of the call sees (slots behind a request's end, other pages) may be
+ * anything, NaN included; keys and values that some query sees have to be
+ * finite.  Deterministic (no atomics).
+ * Supported: D 64, 128 or 256, Hq / Hkv <= 128, block_size 16, 32, 64, 128 or
+ * 256, n_req * ceil(n_q / floor(128 / (Hq / Hkv))) <= 4096, else
+ * THD_ERR_UNSUPPORTED.  (prefix_blocks + max_blocks) * block_size < 2^31,
+ * window >= 0, scale finite and > 0; out of range THD_ERR_INVALID_ARG.
+ * n_req = 0 is a no-op.  Kernel stalls are reported by
+ * thd_attn_shared_prefix_get_error.
+ */
+size_t thd_attn_shared_prefix_workspace_bytes(int n_req, int n_q, int Hq, int Hkv, int D);
+int thd_attn_shared_prefix(const void* q, const void* k_cache, const void* v_cache,
+                           int64_t num_blocks, int block_size,
+                           int64_t block_stride, int64_t token_stride, int64_t head_stride,
+                           const int32_t* prefix_table_or_null, int prefix_blocks,
+                           const int32_t* prefix_len_or_null,
+                           const int32_t* block_tables, int max_blocks, const int32_t* kv_lens,
+                           int n_req, int n_q, int Hq, int Hkv, int D, int window, float scale,
+                           const float* sinks_or_null, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream);
+/* Synchronises the stream; returns and clears the status word of
+ * thd_attn_shared_prefix on the current device. */
+int thd_attn_shared_prefix_get_error(void* stream);
+
 /* ABI version of this header: (major << 16) | minor. */
 int thd_attn_abi_version(void);
 

@@ -23,6 +23,8 @@ import numpy as np
 __all__ = ["thd_attn_fwd", "thd_attn_fwd_noalloc", "thd_attn_fwd_range", "thd_attn_merge",
            "thd_attn_fwd_host",
            "thd_attn_bwd", "thd_attn_bwd_workspace_bytes", "thd_qk_norm_rope",
+           "thd_kv_block_tables", "thd_kv_write", "thd_attn_shared_prefix",
+           "thd_attn_shared_prefix_workspace_bytes", "thd_attn_shared_prefix_get_error",
            "thd_sparse_mla_fwd", "thd_sparse_mla_workspace_bytes", "thd_sparse_mla_get_error",
            "thd_attn_get_error", "thd_attn_noalloc_get_error", "thd_attn_selftest_stall", "thd_attn_plan", "thd_attn_plan_range",
            "thd_attn_plan_range_keys", "ThdAttnError", "library_path", "load_library", "STATUS"]
@@ -124,6 +126,21 @@ def bind(lib):
     lib.thd_qk_norm_rope.argtypes = [vp, vp, i32p, c_int, vp, c_int, c_int, c_int, ctypes.c_float,
                                      ctypes.c_float, c_int, vp]
     lib.thd_qk_norm_rope.restype = c_int
+    i64 = ctypes.c_int64
+    lib.thd_kv_block_tables.argtypes = [vp, vp, c_int, c_int, vp, c_int, vp, i64, vp, vp, i64,
+                                        vp, vp, vp, vp, vp, vp, vp]
+    lib.thd_kv_block_tables.restype = c_int
+    lib.thd_kv_write.argtypes = [vp, vp, i64, i64, vp, i64, c_int, c_int, vp, vp, i64, c_int,
+                                 i64, i64, i64, vp]
+    lib.thd_kv_write.restype = c_int
+    lib.thd_attn_shared_prefix_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, c_int]
+    lib.thd_attn_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
+    lib.thd_attn_shared_prefix.argtypes = [vp, vp, vp, i64, c_int, i64, i64, i64, vp, c_int, vp, vp,
+                                           c_int, vp, c_int, c_int, c_int, c_int, c_int, c_int,
+                                           ctypes.c_float, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.thd_attn_shared_prefix.restype = c_int
+    lib.thd_attn_shared_prefix_get_error.argtypes = [vp]
+    lib.thd_attn_shared_prefix_get_error.restype = c_int
     lib.thd_attn_abi_version.argtypes = []
     lib.thd_attn_abi_version.restype = c_int
     return lib
@@ -555,6 +572,224 @@ def thd_sparse_mla_get_error(stream=None) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return int(load_library().thd_sparse_mla_get_error(ctypes.c_void_p(stream.cuda_stream)))
+
+
+def _check_i32(name, t, shape, device):
+    import torch
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
+
+
+def _check_cuda(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _cache_strides(k_cache, v_cache, device):
+    """Checks a pair of paged caches [blocks, block_size, Hkv, D] and returns
+    (blocks, block_size, Hkv, D, block stride, token stride, head stride)."""
+    import torch
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4:
+            raise ValueError(f"{name} must be a bf16 tensor [blocks, block_size, kv_heads, head_dim] on {device}")
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    nb, bs, Hkv, D = k_cache.shape
+    # the stride of a dimension of one element is never used: any value does
+    dense = (bs * Hkv * D, Hkv * D, D)
+
+    def strides(t):
+        return tuple(d if n <= 1 else s for n, s, d in zip(t.shape[:3], t.stride()[:3], dense))
+    if strides(k_cache) != strides(v_cache) or (D > 1 and (k_cache.stride(3) != 1 or v_cache.stride(3) != 1)):
+        raise ValueError("k_cache and v_cache must have the same strides and a dense head_dim")
+    sb, st, sh = strides(k_cache)
+    # Distinct elements: sorted by stride, every dimension steps over the ones inside it.
+    inside = D
+    for s, n in sorted(((sb, nb), (st, bs), (sh, Hkv))):
+        if n > 1:
+            if s < inside:
+                raise ValueError("the cache's blocks, tokens and heads must not overlap")
+            inside = s * n
+    return nb, bs, Hkv, D, sb, st, sh
+
+
+def thd_kv_block_tables(seq_lens, new_lens, block_tables, free_blocks, free_count, block_size: int,
+                        n_rows: int, first_position=None, seq_lens_out=None, free_count_out=None,
+                        cu_new=None, slots=None, positions=None, refused=None, stream=None):
+    """Pages, block tables, slots and positions of one step, from the requests'
+    lengths (``thd_kv_block_tables`` in thd_attn.h says what happens to each).
+
+    seq_lens, new_lens: int32 CUDA [B]; block_tables: int32 [B, max_blocks] and
+    free_blocks int32 [capacity], both updated in place; free_count: int32 [1];
+    n_rows: rows of the step's packed batch (at least the sum of the new
+    tokens, or requests are refused); first_position: int32 [1] added to the
+    positions (a shared prefix's length) or None.  Returns ``(seq_lens_out,
+    free_count_out, cu_new [B + 1], slots [n_rows], positions [n_rows],
+    refused [1])``; each may be passed in (``seq_lens_out`` may be ``seq_lens``
+    and ``free_count_out`` may be ``free_count``).
+    """
+    import torch
+
+    lib = load_library()
+    _check_cuda("seq_lens", seq_lens)
+    dev = seq_lens.device
+    B, n_rows = seq_lens.shape[0] if seq_lens.dim() == 1 else -1, int(n_rows)
+    if block_tables.dim() != 2 or free_blocks.dim() != 1 or n_rows < 0:
+        raise ValueError("block_tables must be [requests, max_blocks], free_blocks [capacity], n_rows >= 0")
+    M = block_tables.shape[1]
+    for name, t, shape in (("seq_lens", seq_lens, (B,)), ("new_lens", new_lens, (B,)),
+                           ("block_tables", block_tables, (B, M)),
+                           ("free_blocks", free_blocks, tuple(free_blocks.shape)),
+                           ("free_count", free_count, (1,))):
+        _check_i32(name, t, shape, dev)
+    if first_position is not None:
+        _check_i32("first_position", first_position, (1,), dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    outs = []
+    with torch.cuda.stream(stream):
+        for name, t, shape in (("seq_lens_out", seq_lens_out, (B,)), ("free_count_out", free_count_out, (1,)),
+                               ("cu_new", cu_new, (B + 1,)), ("slots", slots, (n_rows,)),
+                               ("positions", positions, (n_rows,)), ("refused", refused, (1,))):
+            if t is None:
+                t = torch.empty(shape, dtype=torch.int32, device=dev)
+            _check_i32(name, t, shape, dev)
+            outs.append(t)
+    with torch.cuda.device(dev):
+        rc = lib.thd_kv_block_tables(
+            seq_lens.data_ptr(), new_lens.data_ptr(), B, int(block_size), block_tables.data_ptr(), M,
+            free_blocks.data_ptr(), free_blocks.numel(), free_count.data_ptr(),
+            first_position.data_ptr() if first_position is not None else None, n_rows,
+            *(t.data_ptr() for t in outs), ctypes.c_void_p(stream.cuda_stream))
+    if rc != 0:
+        raise ThdAttnError(rc, "thd_kv_block_tables")
+    return tuple(outs)
+
+
+def thd_kv_write(k, v, slots, k_cache, v_cache, stream=None):
+    """Write key and value rows into their cache slots (rows whose slot is
+    negative or past the cache are skipped; the other slots must be distinct).
+
+    k, v: bf16 CUDA [rows, Hkv, D], heads dense, rows any multiple of 8
+    elements apart (slices of a fused projection's output); slots: int32
+    [rows]; k_cache, v_cache: bf16 [blocks, block_size, Hkv, D], equal strides,
+    head_dim dense.  Returns ``(k_cache, v_cache)``.
+    """
+    import torch
+
+    lib = load_library()
+    _check_cuda("k", k)
+    dev = k.device
+    nb, bs, Hkv, D, sb, st, sh = _cache_strides(k_cache, v_cache, dev)
+    T = k.shape[0]
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != torch.bfloat16 or t.device != dev or tuple(t.shape) != (T, Hkv, D) or \
+                (T > 0 and not t[0].is_contiguous()):
+            raise ValueError(f"{name} must be a bf16 tensor [rows, {Hkv}, {D}] on {dev} with dense heads")
+    _check_i32("slots", slots, (T,), dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with torch.cuda.device(dev):
+        rc = lib.thd_kv_write(
+            k.data_ptr(), v.data_ptr(), k.stride(0) if T > 1 else Hkv * D, v.stride(0) if T > 1 else Hkv * D,
+            slots.data_ptr(), T, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, sb, st, sh,
+            ctypes.c_void_p(stream.cuda_stream))
+    if rc != 0:
+        raise ThdAttnError(rc, "thd_kv_write")
+    return k_cache, v_cache
+
+
+def thd_attn_shared_prefix(q, k_cache, v_cache, block_tables, kv_lens, prefix_table=None, prefix_len=None,
+                           window: int = 0, scale: Optional[float] = None, sinks=None, out=None, lse=None,
+                           return_lse: bool = True, workspace=None, stream=None):
+    """Attention of a step's new tokens over a shared prefix (once for the
+    batch) and each request's own pages; without a prefix, decoding from the
+    paged cache.
+
+    q: bf16 CUDA [B * n_q, Hq, D], the last n_q tokens of each request's
+    sequence [prefix; own], whose keys and values are all in the cache already;
+    k_cache, v_cache: bf16 [blocks, block_size, Hkv, D] (as ``thd_kv_write``);
+    block_tables: int32 [B, max_blocks]; kv_lens: int32 [B] own tokens (negative:
+    a vacant entry, its rows stay as they are); prefix_table: int32 [blocks of the
+    prefix] and prefix_len: int32 [1], or both None; window, scale, sinks as
+    :func:`thd_attn_fwd`.  ``workspace``: a CUDA byte tensor of at least
+    ``thd_attn_shared_prefix_workspace_bytes(...)``.  Returns ``(out, lse)``
+    (``lse`` is None when ``return_lse`` is False).
+    """
+    import torch
+
+    lib = load_library()
+    _check_cuda("q", q)
+    dev = q.device
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 CUDA tensor [requests * n_q, heads, head_dim]")
+    nb, bs, Hkv, D, sb, st, sh = _cache_strides(k_cache, v_cache, dev)
+    T, Hq = q.shape[0], q.shape[1]
+    if q.shape[2] != D:
+        raise ValueError("q and the cache must share head_dim")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [requests, max_blocks]")
+    B, M = block_tables.shape
+    _check_i32("block_tables", block_tables, (B, M), dev)
+    _check_i32("kv_lens", kv_lens, (B,), dev)
+    if (T % B != 0 if B > 0 else T != 0) or (B > 0 and T == 0):
+        raise ValueError(f"q must hold the same number of rows (at least one) for each of {B} requests")
+    n_q = T // B if B > 0 else 1
+    if (prefix_table is None) != (prefix_len is None):
+        raise ValueError("prefix_table and prefix_len belong together")
+    if prefix_table is not None:
+        _check_i32("prefix_table", prefix_table, (prefix_table.numel(),), dev)
+        _check_i32("prefix_len", prefix_len, (1,), dev)
+        if prefix_table.numel() == 0:
+            prefix_table = prefix_len = None      # nothing but the empty prefix
+    if scale is None:
+        scale = D ** -0.5
+    if sinks is not None:
+        if sinks.dtype != torch.float32 or sinks.device != dev or sinks.numel() != Hq or not sinks.is_contiguous():
+            raise ValueError("sinks must be a contiguous fp32 CUDA tensor of Hq values")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    need = int(lib.thd_attn_shared_prefix_workspace_bytes(B, n_q, Hq, Hkv, D))
+    with torch.cuda.stream(stream):   # what is allocated here is reused in this stream's order
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        if return_lse and lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+    for name, t, dt, shape in (("out", out, torch.bfloat16, (T, Hq, D)), ("lse", lse, torch.float32, (T, Hq))):
+        if t is not None and (t.dtype != dt or t.device != dev or not t.is_contiguous() or tuple(t.shape) != shape):
+            raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape} on {dev}")
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    with torch.cuda.device(dev):
+        rc = lib.thd_attn_shared_prefix(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, sb, st, sh,
+            prefix_table.data_ptr() if prefix_table is not None else None,
+            prefix_table.numel() if prefix_table is not None else 0,
+            prefix_len.data_ptr() if prefix_len is not None else None,
+            block_tables.data_ptr(), M, kv_lens.data_ptr(), B, n_q, Hq, Hkv, D, int(window), float(scale),
+            sinks.data_ptr() if sinks is not None else None, out.data_ptr(),
+            lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), ctypes.c_void_p(stream.cuda_stream))
+    if rc != 0:
+        raise ThdAttnError(rc, "thd_attn_shared_prefix")
+    return out, lse
+
+
+def thd_attn_shared_prefix_workspace_bytes(n_req: int, n_q: int, Hq: int, Hkv: int, D: int) -> int:
+    """Workspace bytes :func:`thd_attn_shared_prefix` needs for n_req requests
+    of n_q query tokens each (partial results; any lengths)."""
+    return int(load_library().thd_attn_shared_prefix_workspace_bytes(int(n_req), int(n_q), int(Hq), int(Hkv), int(D)))
+
+
+def thd_attn_shared_prefix_get_error(stream=None) -> int:
+    """Synchronise the stream and return (and clear) the status word of
+    :func:`thd_attn_shared_prefix` on the current device."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    return int(load_library().thd_attn_shared_prefix_get_error(ctypes.c_void_p(stream.cuda_stream)))
 
 
 def thd_attn_selftest_stall() -> tuple:

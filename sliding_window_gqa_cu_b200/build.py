@@ -17,6 +17,7 @@ LIB = os.path.join(PKG, "libthdattn.so")
 SOURCES = [os.path.join(CSRC, "thd_attn_api.cu"), os.path.join(CSRC, "thd_attn_noalloc.cu"),
            os.path.join(CSRC, "thd_prologue.cu"), os.path.join(CSRC, "thd_sparse_mla.cu"),
            os.path.join(CSRC, "thd_host_pipeline.cu"), os.path.join(CSRC, "thd_attn_merge.cu"),
+           os.path.join(CSRC, "thd_kv_cache.cu"), os.path.join(CSRC, "thd_attn_shared_prefix.cu"),
            os.path.join(CSRC, "scheduler.cpp")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("thd_attn_kernel.cuh", "thd_attn_split_kernel.cuh",
                                                   "thd_attn_bwd_kernels.cuh",

@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(32) thd_stall_selftest_kernel(int* status) {
 
 extern "C" {
 
-int thd_attn_abi_version(void) { return (1 << 16) | 1; }
+int thd_attn_abi_version(void) { return (1 << 16) | 2; }
 
 int thd_attn_selftest_stall(int64_t* waited_ns) {
     if (waited_ns == nullptr) return THD_ERR_INVALID_ARG;
