@@ -1,0 +1,109 @@
+// What the kernels of thd_attn_shared_prefix share: the parameters, the split
+// of the work over the grid, and the layout of partial results.
+//
+// Rows.  The query rows of one kv head are numbered r = token * G + g (token
+// over the whole batch, g the query head inside the group), so a request has
+// RB = n_q * G consecutive rows and a tile of rows may cut anywhere.
+//
+// Work.  A unit is one tile of keys of one item (a row tile of one kv head).
+// A kernel's units are numbered item by item and cut into as many equal
+// consecutive ranges as it has lanes (a CTA, or a group of CTAs in step), so
+// every lane gets the same number whatever the lengths.  What a lane does of
+// one item is a piece.  Its unnormalised output, running maximum (in units of
+// log2) and sum go to the item's home place if the piece holds the item's first
+// tile, else to the CTA's own place (only a lane's first piece can begin inside
+// an item); the merge kernel adds them up in a fixed order.
+//
+// A partial tile is stored as [D / 4][rows][4] fp32 with (maximum, sum) per
+// row beside it: threads that hold neighbouring rows then write, and the merge
+// kernel reads, whole lines.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace thd {
+
+constexpr int kSpLanes = 148;  // CTAs of the prefix kernel (one per SM)
+
+struct SpParams {
+    const __nv_bfloat16* q;
+    const int32_t* prefix_table;
+    const int32_t* prefix_len;
+    const int32_t* tables;
+    const int32_t* kv_lens;
+    const float* sinks;
+    __nv_bfloat16* out;
+    float* lse;
+    int num_blocks, block, block_shift, prefix_blocks, max_blocks;
+    int n_req, n_q, Hq, Hkv, G, window;
+    float scale_log2;
+    int RB;        // rows of a request and kv head
+    int rows;      // rows of a kv head
+    int box_rows;  // tokens of one TMA box of the prefix kernel
+    // prefix kernel
+    int pre_groups;  // row groups of a kv head
+    int pre_width;   // CTAs of a lane (row groups in step)
+    int pre_lanes;
+    float* pre_home;
+    float2* pre_home_ml;
+    float* pre_cont;
+    float2* pre_cont_ml;
+    int* pre_plan;  // [2]: first key tile, number of key tiles
+    // paged kernel
+    int pg_rows;        // rows of its row tile
+    int pg_units;       // row tiles of a request
+    int pg_prefix;      // row tiles of the prefix that it takes (0: none)
+    int pg_ctas;
+    float* own_home;
+    float2* own_home_ml;
+    int2* own_desc;     // first and last CTA of an item
+    float* pgp_home;
+    float2* pgp_home_ml;
+    int2* pgp_desc;
+    float* pg_cont;
+    float2* pg_cont_ml;
+};
+
+// First unit of lane l when `units` are cut into `lanes` ranges (lanes <= units,
+// so that none is empty).
+__device__ __forceinline__ long long lane_begin(long long units, int lanes, int l) {
+    return units * l / lanes;
+}
+
+// The lane that holds unit x: the largest l with units * l / lanes < x + 1.
+__device__ __forceinline__ int lane_of(long long units, int lanes, long long x) {
+    return static_cast<int>(((x + 1) * lanes - 1) / units);
+}
+
+__device__ __forceinline__ int sp_prefix_len(const SpParams& p) {
+    if (p.prefix_len == nullptr) return 0;
+    return min(max(*p.prefix_len, 0), p.prefix_blocks * p.block);
+}
+
+// Own tokens of request b (what its table holds at most); negative: vacant.
+__device__ __forceinline__ int sp_own_len(const SpParams& p, int b) {
+    return min(p.kv_lens[b], p.max_blocks * p.block);
+}
+
+// First key of the sequence [prefix; own] that a query at position pos sees.
+__device__ __forceinline__ int sp_first_key(const SpParams& p, int pos) {
+    return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+}
+
+// First own key that some query of a request of n own tokens sees (the
+// windows of its consecutive queries overlap, so all keys behind it are seen).
+__device__ __forceinline__ int sp_first_own(const SpParams& p, int n) {
+    const int t = n - p.n_q + 1;
+    return p.window > 0 && t > p.window ? t - p.window : 0;
+}
+
+// Tiles of KT own keys that the queries of a request of n own tokens see.
+template <int KT>
+__device__ __forceinline__ int sp_own_tiles(const SpParams& p, int n) {
+    return n > 0 ? (n - 1) / KT + 1 - sp_first_own(p, n) / KT : 0;
+}
+
+}  // namespace thd

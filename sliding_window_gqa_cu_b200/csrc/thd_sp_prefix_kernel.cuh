@@ -1,0 +1,609 @@
+// The shared prefix on the tensor cores: every query row of the batch against
+// the pages of the prefix, each key tile read once for NT * 128 rows.
+//
+// With P prefix keys and R = tokens * G rows per kv head this is two matrix
+// products of 2 R P D operations each per kv head around a softmax, so with
+// many rows the tensor core bounds it (a 128 x 128 tile at D = 128: 2 * 512
+// cycles) next to the exponential unit (16 a cycle: 1024 cycles a tile).
+// NT = 2 row tiles per CTA (D <= 128) take turns: while one tile's scores are
+// in the softmax the tensor core works on the other's.  At D = 256 the two
+// accumulators would fill TMEM, so one row tile with two score buffers does
+// the same.
+//
+// Work split: groups of NT * 128 rows; `pre_width` groups of a kv head walk the
+// same keys in step (one CTA each, so that K and V come from L2 for all but the
+// first), and the sequence (bundle of groups, kv head, key tile) is cut into
+// equal ranges, one per lane of CTAs.
+//
+// Warps: 4 NT softmax warps (thread = row), a TMA producer, an MMA issuer.
+// The kernel leaves registers and, at D <= 128, shared memory for a CTA of the
+// paged kernel on the same SM: that one is bound by memory.  For that a
+// thread holds half a row of scores at a time; the first half is read from TMEM
+// twice (once for the maximum).
+#pragma once
+
+#include "thd_attn_kernel.cuh"
+#include "thd_sp_common.cuh"
+
+namespace thd {
+
+template <int D_>
+struct PrefixConfig {
+    static constexpr int D = D_;
+    static constexpr int NT = D == 256 ? 1 : 2;   // row tiles of a CTA
+    static constexpr int NSB = D == 256 ? 2 : 1;  // score buffers of a row tile
+    static constexpr int BN = 128;                // keys of a tile
+    static constexpr int SC = D < 128 ? D : 128;  // columns of a ring slot
+    static constexpr int SUB = D / SC;            // slots of a K or V tile
+    static constexpr int CH = SC / 64;            // 128-byte chunks of a slot row
+    static constexpr int NSLOT = D == 64 ? 6 : D == 128 ? 3 : 4;
+    static constexpr int BOX_BYTES = BN * 128;    // one chunk of a slot
+    static constexpr int SLOT_BYTES = BN * SC * 2;
+    static constexpr int Q_TILE_BYTES = 128 * D * 2;
+    static constexpr int SOFTMAX_WARPS = 4 * NT;
+    static constexpr int PRODUCER_WARP = SOFTMAX_WARPS;
+    static constexpr int MMA_WARP = SOFTMAX_WARPS + 1;
+    static constexpr int THREADS = (SOFTMAX_WARPS + 2) * 32;
+    // Threads that the register budget is made for: 128 registers a thread leave
+    // a quarter of the registers to a CTA of the paged kernel.
+    static constexpr int BOUND = D == 256 ? 384 : 512;
+
+    static constexpr int TMEM_O = NT * NSB * BN;
+    static_assert(TMEM_O + NT * D <= 512, "TMEM budget exceeded");
+
+    static constexpr int B_Q_FULL = 0;                        // [NT]
+    static constexpr int B_SLOT_FULL = B_Q_FULL + NT;
+    static constexpr int B_SLOT_EMPTY = B_SLOT_FULL + NSLOT;
+    static constexpr int B_S_FULL = B_SLOT_EMPTY + NSLOT;     // [NT][NSB]
+    static constexpr int B_P_FULL = B_S_FULL + NT * NSB;      // [NT][2]: keys 64.. first, then 0..63
+    static constexpr int B_O_FULL = B_P_FULL + 2 * NT;        // [NT]
+    static constexpr int B_DRAIN = B_O_FULL + NT;
+    static constexpr int NUM_BARS = B_DRAIN + 1;
+
+    static constexpr int SMEM_SLOTS = NT * Q_TILE_BYTES;
+    static constexpr int SMEM_BAR = SMEM_SLOTS + NSLOT * SLOT_BYTES;
+    static constexpr int SMEM_MIN = SMEM_BAR + NUM_BARS * 8;  // [warp]: least own length
+    static constexpr int SMEM_TMEM_SLOT = SMEM_MIN + 16 * 4;
+    static constexpr int SMEM_ABORT = SMEM_TMEM_SLOT + 4;
+    static constexpr int SMEM_BYTES = SMEM_ABORT + 4;
+};
+
+// One CTA's share of one item.
+struct PrefixPiece {
+    int h, row0, tiles;       // kv head, first row, active row tiles
+    int kt, n;                // first key tile and how many
+    int lo;                   // first key that some row sees
+    bool home;                // holds the item's first tile
+    int group;                // row group
+};
+
+// Walks the pieces of a CTA; called by whole warps, which all get the same.
+template <class C>
+struct PrefixWalk {
+    long long x, x1;
+    int member, first_tile, n_tiles, prefix, n_items;
+
+    __device__ __forceinline__ bool next(const SpParams& p, PrefixPiece& pc) {
+        while (x < x1) {
+            const int item = static_cast<int>(x / n_tiles);
+            const int at = static_cast<int>(x - static_cast<long long>(item) * n_tiles);
+            const int cnt = static_cast<int>(min(static_cast<long long>(n_tiles - at), x1 - x));
+            x += cnt;
+            pc.h = item % p.Hkv;
+            pc.group = item / p.Hkv * p.pre_width + member;
+            if (pc.group >= p.pre_groups) continue;
+            pc.row0 = pc.group * (C::NT * 128);
+            const int left = p.rows - pc.row0;
+            pc.tiles = C::NT == 2 && left > 128 ? 2 : 1;
+            pc.home = at == 0;
+            int lo = 0;
+            if (p.window > 0) {
+                // least own length of the group's requests
+                const int last = min(left, C::NT * 128) - 1;
+                const int b0 = pc.row0 / p.RB, b1 = (pc.row0 + last) / p.RB;
+                int n = 0x7fffffff;
+                for (int b = b0 + static_cast<int>(threadIdx.x & 31); b <= b1; b += 32) {
+                    const int len = sp_own_len(p, b);
+                    if (len >= 0) n = min(n, len);
+                }
+                n = __reduce_min_sync(0xffffffffu, n);
+                lo = n == 0x7fffffff ? prefix : sp_first_key(p, prefix + n - p.n_q);
+            }
+            pc.lo = lo;
+            const int k0 = max(first_tile + at, lo / C::BN);
+            pc.kt = k0;
+            pc.n = max(0, first_tile + at + cnt - k0);
+            if (lo >= prefix) pc.n = 0;
+            return true;
+        }
+        return false;
+    }
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::BOUND, 1)
+thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                     const SpParams p, int* status) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_addr(smem);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    launch_dependents();
+
+    auto bar = [&](int idx) -> uint32_t { return sbase + C::SMEM_BAR + 8u * idx; };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::SMEM_ABORT);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SMEM_TMEM_SLOT);
+    int* warp_min = reinterpret_cast<int*>(smem + C::SMEM_MIN);
+
+    if (threadIdx.x == 0) {
+        for (int q = 0; q < C::NT; ++q) {
+            mbar_init(bar(C::B_Q_FULL + q), 4);
+            mbar_init(bar(C::B_P_FULL + 2 * q), 4);
+            mbar_init(bar(C::B_P_FULL + 2 * q + 1), 4);
+            mbar_init(bar(C::B_O_FULL + q), 1);
+        }
+        for (int s = 0; s < C::NSLOT; ++s) {
+            mbar_init(bar(C::B_SLOT_FULL + s), 1);
+            mbar_init(bar(C::B_SLOT_EMPTY + s), 1);
+        }
+        for (int i = 0; i < C::NT * C::NSB; ++i) mbar_init(bar(C::B_S_FULL + i), 1);
+        mbar_init(bar(C::B_DRAIN), 1);
+        int bad = *reinterpret_cast<volatile int*>(status) != 0 ? 1 : 0;
+        if ((sbase & 1023u) != 0) {  // the swizzled tiles need it
+            atomicCAS(status, 0, kStatusBadItem);
+            bad = 1;
+        }
+        *abort_flag = bad;
+        fence_barrier_init();
+    }
+    if (warp == C::MMA_WARP) {
+        tmem_alloc(smem_addr(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    // Key tiles that any row can see.
+    const int P = sp_prefix_len(p);
+    {
+        int n = 0x7fffffff;
+        if (p.window > 0)
+            for (int b = threadIdx.x; b < p.n_req; b += C::THREADS) {
+                const int len = sp_own_len(p, b);
+                if (len >= 0) n = min(n, len);
+            }
+        n = __reduce_min_sync(0xffffffffu, n);
+        if (lane == 0) warp_min[warp] = n;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const bool skip = *abort_flag != 0;
+
+    PrefixWalk<C> walk;
+    {
+        int lo = 0;
+        if (p.window > 0) {
+            int n = 0x7fffffff;
+            for (int w = 0; w < C::THREADS / 32; ++w) n = min(n, warp_min[w]);
+            lo = n == 0x7fffffff ? P : sp_first_key(p, P + n - p.n_q);
+        }
+        walk.first_tile = lo / C::BN;
+        walk.n_tiles = lo < P ? (P - 1) / C::BN + 1 - walk.first_tile : 0;
+        walk.prefix = P;
+        walk.member = blockIdx.x % p.pre_width;
+        const int my_lane = blockIdx.x / p.pre_width;
+        const long long units = static_cast<long long>((p.pre_groups + p.pre_width - 1) / p.pre_width) * p.Hkv *
+                                walk.n_tiles;
+        const int lanes = static_cast<int>(min(units, static_cast<long long>(p.pre_lanes)));
+        walk.x = my_lane < lanes ? lane_begin(units, lanes, my_lane) : 0;
+        walk.x1 = my_lane < lanes ? lane_begin(units, lanes, my_lane + 1) : 0;
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            p.pre_plan[0] = walk.first_tile;
+            p.pre_plan[1] = walk.n_tiles;
+        }
+    }
+    PrefixPiece pc;
+
+    if (warp == C::PRODUCER_WARP) {
+        // ------------------------------------------------------ TMA producer
+        if (!skip) {
+            if (lane == 0) {
+                tma_prefetch_desc(&tmap_k);
+                tma_prefetch_desc(&tmap_v);
+            }
+            const int boxes = C::BN / p.box_rows;  // boxes of a chunk, one lane each
+            const int box = lane < boxes ? lane : 0;
+            int pos = 0, issued = 0;
+            bool ok = true;
+            // Page of this lane's box of key tile kt (one past the cache if there is none).
+            auto page_of = [&](int kt) -> int {
+                const int idx = (kt * C::BN + box * p.box_rows) >> p.block_shift;
+                int id = -1;
+                if (idx < p.prefix_blocks) id = p.prefix_table[idx];
+                return id >= 0 && id < p.num_blocks ? id : p.num_blocks;
+            };
+            auto load_tile = [&](const CUtensorMap* map, int kt, int id, int h) {
+                const int row = (kt * C::BN + box * p.box_rows) & (p.block - 1);
+                for (int s = 0; s < C::SUB && ok; ++s) {
+                    const int slot = pos % C::NSLOT;
+                    ok = warp_wait(bar(C::B_SLOT_EMPTY + slot), ((pos / C::NSLOT) & 1) ^ 1, abort_flag, status);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(C::B_SLOT_FULL + slot), C::SLOT_BYTES);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const uint32_t dst = sbase + C::SMEM_SLOTS + slot * C::SLOT_BYTES + box * p.box_rows * 128;
+#pragma unroll
+                        for (int c = 0; c < C::CH; ++c)
+                            tma_load_4d(dst + c * C::BOX_BYTES, map, bar(C::B_SLOT_FULL + slot),
+                                        s * C::SC + c * 64, h, row, id);
+                    }
+                    issued = ++pos;
+                }
+            };
+            while (ok && walk.next(p, pc)) {
+                if (pc.n == 0) continue;
+                // Consumption order: K(0) .. K(NSB - 1), then V(j), K(j + NSB).
+                int next_id = page_of(pc.kt);
+                int ids[C::NSB];
+                for (int jj = 0; jj < C::NSB && jj < pc.n && ok; ++jj) {
+                    const int id = next_id;
+                    if (jj + 1 < pc.n) next_id = page_of(pc.kt + jj + 1);
+                    load_tile(&tmap_k, pc.kt + jj, id, pc.h);
+                    if constexpr (C::NSB == 2) ids[jj] = id; else ids[0] = id;
+                }
+                for (int j = 0; j < pc.n && ok; ++j) {
+                    load_tile(&tmap_v, pc.kt + j, ids[0], pc.h);
+                    const int jn = j + C::NSB;
+                    int id = 0;
+                    if (jn < pc.n && ok) {
+                        id = next_id;
+                        if (jn + 1 < pc.n) next_id = page_of(pc.kt + jn + 1);
+                        load_tile(&tmap_k, pc.kt + jn, id, pc.h);
+                    }
+                    if constexpr (C::NSB == 2) {
+                        ids[0] = ids[1];
+                        ids[1] = id;
+                    } else {
+                        ids[0] = id;
+                    }
+                }
+            }
+            if (!ok && lane == 0)  // let the loads in flight land before the CTA ends
+                for (int q = issued > C::NSLOT ? issued - C::NSLOT : 0; q < issued; ++q)
+                    drain_wait(bar(C::B_SLOT_FULL + q % C::NSLOT), (q / C::NSLOT) & 1);
+        }
+        __syncwarp();
+    } else if (warp == C::MMA_WARP) {
+        // -------------------------------------------------------- MMA issuer
+        if (!skip) {
+            constexpr uint32_t idesc_qk = idesc_bf16_f32(128, C::BN, false);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, C::SC, true);
+            const uint64_t dq0 = smem_desc_sw128(sbase, 16, 1024);
+            const uint64_t dk0 = smem_desc_sw128(sbase + C::SMEM_SLOTS, 16, 1024);
+            const uint64_t dv0 = smem_desc_sw128(sbase + C::SMEM_SLOTS, C::BOX_BYTES, 1024);
+            // Part s of S = Q K^T: head-dim columns [s SC, (s + 1) SC).
+            auto issue_qk = [&](int q, int b, int s, int slot) {
+                const uint32_t d_tmem = tmem_base + (q * C::NSB + b) * C::BN;
+                const uint64_t dq = dq0 + ((q * C::Q_TILE_BYTES + s * C::CH * C::BOX_BYTES) >> 4);
+                const uint64_t dk = dk0 + ((slot * C::SLOT_BYTES) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < C::SC / 16; ++kk) {
+                    const uint32_t o = ((kk >> 2) * C::BOX_BYTES + (kk & 3) * 32) >> 4;
+                    mma_bf16_ss(d_tmem, dq + o, dk + o, idesc_qk, s > 0 || kk > 0 ? 1u : 0u);
+                }
+            };
+            // Part s of O += P V (columns [s SC, ..)) over keys [64 half, 64 half + 64),
+            // whose P lies in the score columns [64 half, 64 half + 32).
+            auto issue_pv = [&](int q, int b, int s, int slot, int half, bool acc) {
+                const uint32_t d_tmem = tmem_base + C::TMEM_O + q * C::D + s * C::SC;
+                const uint32_t p_tmem = tmem_base + (q * C::NSB + b) * C::BN + half * 64;
+                const uint64_t dv = dv0 + ((slot * C::SLOT_BYTES + half * 64 * 128) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_bf16_ts(d_tmem, p_tmem + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_pv,
+                                acc || kk > 0 ? 1u : 0u);
+            };
+            int pos = 0, pieces[2] = {0, 0}, done[2] = {0, 0};  // per row tile
+            bool ok = true;
+            auto wait = [&](int idx, uint32_t parity) -> bool {
+                return mbar_wait(bar(idx), parity, abort_flag, status, kStatusTimeout);
+            };
+            auto wait_slot = [&](int at) -> bool {
+                return wait(C::B_SLOT_FULL + at % C::NSLOT, (at / C::NSLOT) & 1);
+            };
+            while (walk.next(p, pc)) {
+                if (pc.n == 0 || !ok) continue;
+                if (lane == 0) {
+                    const int n = pc.n;
+                    for (int q = 0; q < pc.tiles && ok; ++q) ok = wait(C::B_Q_FULL + q, pieces[q] & 1);
+                    // K tile of step jj at ring position `pos`: one part per slot
+                    auto qk = [&](int jj) {
+                        for (int s = 0; s < C::SUB && ok; ++s) {
+                            ok = wait_slot(pos + s);
+                            if (!ok) return;
+                            tc_fence_after();
+                            for (int q = 0; q < pc.tiles; ++q)
+                                issue_qk(q, (done[q] + jj) % C::NSB, s, (pos + s) % C::NSLOT);
+                            if (s == C::SUB - 1)
+                                for (int q = 0; q < pc.tiles; ++q)
+                                    mma_commit(bar(C::B_S_FULL + q * C::NSB + (done[q] + jj) % C::NSB));
+                            mma_commit(bar(C::B_SLOT_EMPTY + (pos + s) % C::NSLOT));
+                        }
+                    };
+                    for (int jj = 0; jj < C::NSB && jj < n && ok; ++jj) {
+                        qk(jj);
+                        pos += C::SUB;
+                    }
+                    for (int j = 0; j < n && ok; ++j) {
+                        const bool more = j + C::NSB < n;
+                        const int vpos = pos, kpos = pos + C::SUB;
+                        if constexpr (C::NSB == 1) {
+                            // PV(j) and QK(j + 1) of a row tile go out as one run with one
+                            // commit: S(j + 1) ready also says that O holds PV(j).
+                            ok = wait_slot(vpos);
+                            for (int q = 0; q < pc.tiles && ok; ++q) {
+                                for (int half = 1; half >= 0 && ok; --half) {
+                                    ok = wait(C::B_P_FULL + 2 * q + half, (done[q] + j) & 1);
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                    issue_pv(q, 0, 0, vpos % C::NSLOT, half, j > 0 || half == 0);
+                                }
+                                if (!ok) break;
+                                if (more) {
+                                    if (q == 0) ok = wait_slot(kpos);
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                    issue_qk(q, 0, 0, kpos % C::NSLOT);
+                                    mma_commit(bar(C::B_S_FULL + q));
+                                } else {
+                                    mma_commit(bar(C::B_O_FULL + q));
+                                }
+                            }
+                            if (!ok) break;
+                            mma_commit(bar(C::B_SLOT_EMPTY + vpos % C::NSLOT));
+                            if (more) mma_commit(bar(C::B_SLOT_EMPTY + kpos % C::NSLOT));
+                            pos += more ? 2 : 1;
+                        } else {
+                            const int b = (done[0] + j) % C::NSB;
+                            for (int half = 1; half >= 0 && ok; --half)
+                                ok = wait(C::B_P_FULL + half, (done[0] + j) & 1);
+                            for (int s = 0; s < C::SUB && ok; ++s) {
+                                ok = wait_slot(vpos + s);
+                                if (!ok) break;
+                                tc_fence_after();
+                                issue_pv(0, b, s, (vpos + s) % C::NSLOT, 1, j > 0);
+                                issue_pv(0, b, s, (vpos + s) % C::NSLOT, 0, true);
+                                if (s == C::SUB - 1) mma_commit(bar(C::B_O_FULL));
+                                mma_commit(bar(C::B_SLOT_EMPTY + (vpos + s) % C::NSLOT));
+                            }
+                            pos += C::SUB;
+                            if (ok && more) {
+                                qk(j + C::NSB);
+                                pos += C::SUB;
+                            }
+                        }
+                    }
+                    for (int q = 0; q < pc.tiles; ++q) {
+                        ++pieces[q];
+                        done[q] += n;
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            }
+            if (lane == 0) {
+                mma_commit(bar(C::B_DRAIN));
+                drain_wait(bar(C::B_DRAIN), 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int q = warp >> 2;
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t o_tmem = lane_base + C::TMEM_O + q * C::D;
+        const float sl2 = p.scale_log2;
+        const int valid_pages_lane = (lane * 16) >> p.block_shift;  // page of 16-key group `lane` of a tile
+        constexpr float kTau = 8.0f;  // rescale O only when the maximum grows by more than 2^8
+        int pos = 0, pieces = 0, done = 0;
+        bool ok = !skip;
+        while (ok && walk.next(p, pc)) {
+            const int base_pos = pos;
+            pos += 2 * C::SUB * pc.n;
+            if (q >= pc.tiles) continue;
+            const int r = pc.row0 + q * 128 + row;
+            int jlo = pc.lo, jhi = P - 1;  // keys of the prefix that the row sees (unused rows: all)
+            if (r < p.rows) {
+                const int b = r / p.RB;
+                const int n_own = sp_own_len(p, b);
+                if (n_own >= 0) {
+                    const int at = P + n_own - p.n_q + (r - b * p.RB) / p.G;
+                    jlo = sp_first_key(p, at);
+                    jhi = min(at, P - 1);
+                }
+            }
+            float m_ref = -INFINITY, l = 0.0f;
+            float* home;
+            float2* ml;
+            if (pc.home) {
+                const int64_t tile = (static_cast<int64_t>(pc.h) * p.pre_groups + pc.group) * C::NT + q;
+                home = p.pre_home + tile * (128 * C::D);
+                ml = p.pre_home_ml + tile * 128;
+            } else {
+                const int64_t tile = static_cast<int64_t>(blockIdx.x) * C::NT + q;
+                home = p.pre_cont + tile * (128 * C::D);
+                ml = p.pre_cont_ml + tile * 128;
+            }
+            if (pc.n > 0) {
+                // Q rows into shared memory, 128-byte swizzled: a warp its own 32 rows.
+                {
+                    constexpr int PER = C::D / 8;  // 16-byte pieces of a row
+                    const int r_first = pc.row0 + q * 128 + (warp & 3) * 32;
+#pragma unroll 4
+                    for (int i = lane; i < 32 * PER; i += 32) {
+                        const int rr = i / PER, c = i % PER;
+                        const int g_row = r_first + rr;
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (g_row < p.rows) {
+                            const int t = g_row / p.G;
+                            x = *reinterpret_cast<const uint4*>(
+                                p.q + (static_cast<int64_t>(t) * p.Hq + pc.h * p.G + (g_row - t * p.G)) * C::D + c * 8);
+                        }
+                        const int lr = (warp & 3) * 32 + rr;
+                        st_shared_v4(sbase + q * C::Q_TILE_BYTES + (c >> 3) * C::BOX_BYTES + lr * 128 +
+                                         (((c & 7) ^ (lr & 7)) << 4),
+                                     x.x, x.y, x.z, x.w);
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_Q_FULL + q));
+                }
+                // Bit i: the 16-key group i of tile kt lies in a page of the cache.
+                auto load_id = [&](int kt) -> int {
+                    const int idx = ((kt * C::BN) >> p.block_shift) + valid_pages_lane;
+                    return lane < 8 && idx < p.prefix_blocks ? p.prefix_table[idx] : -1;
+                };
+                int id = load_id(pc.kt);
+                for (int j = 0; j < pc.n; ++j) {
+                    const int t = done + j;
+                    const int b = t % C::NSB;
+                    const int key0 = (pc.kt + j) * C::BN;
+                    const uint32_t pages =
+                        __ballot_sync(0xffffffffu, lane < 8 && id >= 0 && id < p.num_blocks) & 0xffu;
+                    if (j + 1 < pc.n) id = load_id(pc.kt + j + 1);
+                    ok = warp_wait(bar(C::B_S_FULL + q * C::NSB + b), (t / C::NSB) & 1, abort_flag, status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t s_tmem = lane_base + (q * C::NSB + b) * C::BN;
+                    const bool all = __all_sync(0xffffffffu, key0 >= jlo && key0 + C::BN - 1 <= jhi) && pages == 0xffu;
+                    const int c_lo = jlo > key0 ? (jlo - key0 < C::BN ? jlo - key0 : C::BN) : 0;
+                    const int c_hi = jhi - key0;
+                    // Scores of columns [c0, c0 + 32); hidden ones become -inf.
+                    uint32_t raw[64];
+                    float sv[64];
+                    auto load64 = [&](int c0) {
+                        tmem_ld32(s_tmem + c0, *reinterpret_cast<uint32_t(*)[32]>(&raw[0]));
+                        tmem_ld32(s_tmem + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[32]));
+                        tmem_wait_ld();
+                        reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&raw[0]));
+                        reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&raw[32]));
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(raw[c]);
+                        if (!all) {
+#pragma unroll
+                            for (int c = 0; c < 64; ++c)
+                                if (c0 + c < c_lo || c0 + c > c_hi || !((pages >> ((c0 + c) >> 4)) & 1u)) sv[c] = -INFINITY;
+                        }
+                    };
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto max64 = [&]() {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2) mx[(c >> 1) & 3] = max3f(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
+                    };
+                    load64(0);
+                    max64();
+                    load64(64);
+                    max64();
+                    const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+
+                    float alpha = 1.0f;
+                    bool rescale = false;
+                    if (j == 0) {
+                        m_ref = m_tile;
+                    } else if (m_tile > m_ref + kTau) {
+                        alpha = ex2_approx(m_ref - m_tile);
+                        m_ref = m_tile;
+                        rescale = true;
+                    }
+                    l *= alpha;
+                    const float neg_m = m_ref == -INFINITY ? 0.0f : -m_ref;
+                    // O has to hold PV(j - 1) before it is rescaled and before P(j) is
+                    // published.  With one score buffer S(j) ready says so.
+                    if (C::NSB == 2 && j > 0) {
+                        ok = warp_wait(bar(C::B_O_FULL + q), (t - 1) & 1, abort_flag, status);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    // Values of keys that no row of the group sees may be anything:
+                    // zero them, as 0 * NaN would stay NaN.  (Whatever held V(j)'s slots
+                    // before has been consumed by now, so their phase is this one's.)
+                    if (key0 < pc.lo || key0 + C::BN > P) {
+                        const int v_tiles = min(pc.n, C::NSB + j) + j;  // K and V tiles before V(j)
+#pragma unroll 1
+                        for (int s = 0; s < C::SUB && ok; ++s) {
+                            const int at = base_pos + C::SUB * v_tiles + s;
+                            ok = warp_wait(bar(C::B_SLOT_FULL + at % C::NSLOT), (at / C::NSLOT) & 1, abort_flag, status);
+                            if (!ok) break;
+                            if (key0 + row < pc.lo || key0 + row >= P) {
+                                const uint32_t dst = sbase + C::SMEM_SLOTS + (at % C::NSLOT) * C::SLOT_BYTES + row * 128;
+                                for (int c = 0; c < C::CH; ++c)
+#pragma unroll
+                                    for (int u = 0; u < 8; ++u)
+                                        st_shared_v4(dst + c * C::BOX_BYTES + u * 16, 0, 0, 0, 0);
+                            }
+                        }
+                        if (!ok) break;
+                        fence_proxy_async_smem();
+                    }
+                    if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+                        for (int c = 0; c < C::D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(o_tmem + c * 32, o);
+                            tmem_wait_ld();
+                            reg_fence32(o);
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+                            tmem_st32(o_tmem + c * 32, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    const float2 sl2x2 = make_float2(sl2, sl2);
+                    const float2 negm2 = make_float2(neg_m, neg_m);
+                    float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+                    // P of keys 64.. over the score columns [64, 96), which are in registers.
+                    exp_and_store_p<0, 2, 64, 0>(sv, sl2x2, negm2, s_tmem + 64, acc0, acc1);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_P_FULL + 2 * q + 1));
+                    load64(0);
+                    exp_and_store_p<0, 2, 64, 0>(sv, sl2x2, negm2, s_tmem, acc0, acc1);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_P_FULL + 2 * q));
+                    l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                }
+                if (ok)
+                    ok = warp_wait(bar(C::B_O_FULL + q), C::NSB == 1 ? pieces & 1 : (done + pc.n - 1) & 1, abort_flag,
+                                   status);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < C::D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(o_tmem + c * 32, o);
+                    tmem_wait_ld();
+                    reg_fence32(o);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        *reinterpret_cast<uint4*>(home + ((c * 8 + u) * 128 + row) * 4) =
+                            make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                }
+                ++pieces;
+                done += pc.n;
+            }
+            ml[row] = make_float2(m_ref, l);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+}  // namespace thd
