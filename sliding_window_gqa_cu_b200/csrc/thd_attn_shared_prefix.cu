@@ -19,6 +19,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/thd_attn.h"
 #include "thd_sp_paged_kernel.cuh"
@@ -34,102 +35,140 @@ using thd::SpParams;
 __device__ int g_sp_status;
 
 // Adds up the parts of every row in a fixed order.  A warp takes 8 consecutive
-// rows of a kv head x 64 columns; a thread one row and four groups of four
-// columns.  Reads the parts once (a few MB): a small fraction of the step.
+// rows of a kv head x 32 columns; a thread one row and two groups of four
+// columns.  The parts are a few MB in L2; a row that many CTAs worked on has
+// many of them, so four are loaded at a time.
 template <int D>
 __global__ void __launch_bounds__(256) thd_sp_merge_kernel(const SpParams p) {
     constexpr int NT = thd::PrefixConfig<D>::NT;
-    constexpr int KT = thd::PagedConfig<D, 1>::KT;
     const int lane = threadIdx.x & 31;
     const int groups = (p.rows + 7) / 8;
     const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int h = static_cast<int>(w / groups);
     const int r = static_cast<int>(w - static_cast<int64_t>(h) * groups) * 8 + (lane & 7);
-    const int c4 = blockIdx.y * 16 + (lane >> 3);
+    const int c4 = blockIdx.y * 8 + (lane >> 3);
     thd::wait_for_previous_grid();
     if (h >= p.Hkv || r >= p.rows) return;
     const int b = r / p.RB, rr = r - b * p.RB;
     const int n = thd::sp_own_len(p, b);
     if (n < 0) return;
 
-    // Up to two sources (the prefix and the request's pages), each a home place
-    // and the own places of CTAs first, first + step, ... < end.
-    struct Source {
-        const float* home;
-        const float2* home_ml;
-        const float* cont;
-        const float2* cont_ml;
-        int64_t cont_tile;
-        int rows, row, cont_row, cont_rows, first, end, step;
-    } src[2];
-    int n_src = 0;
-    const int pre_tiles = p.pre_lanes > 0 || p.pg_prefix > 0 ? p.pre_plan[1] : 0;
-    if (pre_tiles > 0 && p.pre_lanes > 0) {
-        const int tile = r >> 7, group = tile / NT;
+    // Runs of parts: the home place and the own places of the following
+    // workers, of the prefix and of the request's pages.
+    struct Run {
+        const float* part;   // of this thread's row
+        const float2* ml;
+        int64_t part_step, ml_step;
+        int n, rows;
+    } run[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) run[i].n = 0;
+    const int pre_tiles = p.pre_lanes > 0 || p.pg_prefix > 0 ? p.plan->pre_tiles : 0;
+    // Parts of the item whose keys begin at unit x, `count` units of keys, in
+    // `units` units over `lanes` workers, `step` CTAs to a worker.
+    auto runs = [&](Run& home, Run& cont, long long units, int lanes, long long x, int count, int step, int member,
+                    int tile_rows, int tile_row) {
+        const int first = thd::lane_of(units, lanes, x), last = thd::lane_of(units, lanes, x + count - 1);
+        home.n = 1;
+        home.part_step = home.ml_step = 0;
+        cont.n = last - first;
+        cont.rows = tile_rows;
+        const int64_t at = (static_cast<int64_t>(first + 1) * step + member) * tile_rows;
+        cont.part += at * D;
+        cont.ml += at + tile_row;
+        cont.part_step = static_cast<int64_t>(step) * tile_rows * D;
+        cont.ml_step = static_cast<int64_t>(step) * tile_rows;
+    };
+    const bool quads = p.pre_lanes > 0;  // the prefix's parts are [D / 4][rows][4]
+    if (pre_tiles > 0 && quads) {
+        const int tile = r >> 7, group = tile / NT, q = tile - group * NT;
         const long long units = static_cast<long long>((p.pre_groups + p.pre_width - 1) / p.pre_width) * p.Hkv * pre_tiles;
         const int lanes = static_cast<int>(min(units, static_cast<long long>(p.pre_lanes)));
-        const long long x = (static_cast<long long>(group / p.pre_width) * p.Hkv + h) * pre_tiles;
-        const int member = group % p.pre_width, q = tile - group * NT;
         const int64_t at = (static_cast<int64_t>(h) * p.pre_groups + group) * NT + q;
-        src[n_src++] = Source{p.pre_home + at * (128 * D), p.pre_home_ml + at * 128,
-                              p.pre_cont + static_cast<int64_t>(q) * (128 * D), p.pre_cont_ml + q * 128,
-                              static_cast<int64_t>(NT) * 128, 128, r & 127, r & 127, 128,
-                              (thd::lane_of(units, lanes, x) + 1) * p.pre_width + member,
-                              thd::lane_of(units, lanes, x + pre_tiles - 1) * p.pre_width + member + 1, p.pre_width};
+        run[0].part = p.pre_home + at * (128 * D) + (r & 127) * 4;
+        run[0].ml = p.pre_home_ml + at * 128 + (r & 127);
+        run[0].rows = 128;
+        run[1].part = p.pre_cont + (r & 127) * 4 + static_cast<int64_t>(q) * (128 * D);
+        run[1].ml = p.pre_cont_ml + q * 128;
+        runs(run[0], run[1], units, lanes, (static_cast<long long>(group / p.pre_width) * p.Hkv + h) * pre_tiles, pre_tiles,
+             p.pre_width, group % p.pre_width, NT * 128, r & 127);
+        run[1].rows = 128;
     } else if (pre_tiles > 0) {
         const int item = r / p.pg_rows * p.Hkv + h, row = r % p.pg_rows;
-        const int2 d = p.pgp_desc[item];
-        src[n_src++] = Source{p.pgp_home + static_cast<int64_t>(item) * p.pg_rows * D,
-                              p.pgp_home_ml + static_cast<int64_t>(item) * p.pg_rows, p.pg_cont, p.pg_cont_ml,
-                              p.pg_rows, p.pg_rows, row, row, p.pg_rows, d.x + 1, d.y + 1, 1};
+        run[0].part = p.pgp_home + static_cast<int64_t>(item) * p.pg_rows * D + row;
+        run[0].ml = p.pgp_home_ml + static_cast<int64_t>(item) * p.pg_rows + row;
+        run[0].rows = p.pg_rows;
+        run[1].part = p.pg_cont + row;
+        run[1].ml = p.pg_cont_ml;
+        runs(run[0], run[1], p.plan->pg_units, p.plan->pg_lanes, p.pgp_desc[item] + thd::kItemUnits, pre_tiles, 1, 0,
+             p.pg_rows, row);
     }
-    if (thd::sp_own_tiles<KT>(p, n) > 0) {
+    const int own = p.pg_slice == 32 ? thd::sp_own_slices<32>(p, n) : thd::sp_own_slices<16>(p, n);
+    if (own > 0) {
         const int64_t bh = static_cast<int64_t>(b) * p.Hkv + h;
-        const int2 d = p.own_desc[bh * p.pg_units + rr / p.pg_rows];
-        src[n_src++] = Source{p.own_home + bh * p.RB * D, p.own_home_ml + bh * p.RB, p.pg_cont, p.pg_cont_ml,
-                              p.pg_rows, p.RB, rr, rr % p.pg_rows, p.pg_rows, d.x + 1, d.y + 1, 1};
+        run[2].part = p.own_home + bh * p.RB * D + rr;
+        run[2].ml = p.own_home_ml + bh * p.RB + rr;
+        run[2].rows = p.RB;
+        run[3].part = p.pg_cont + rr % p.pg_rows;
+        run[3].ml = p.pg_cont_ml;
+        runs(run[2], run[3], p.plan->pg_units, p.plan->pg_lanes,
+             p.own_desc[bh * p.pg_units + rr / p.pg_rows] + thd::kItemUnits, own, 1, 0, p.pg_rows, rr % p.pg_rows);
     }
     const int g = r % p.G, head = h * p.G + g;
     const int64_t t = r / p.G;
-    float m = -INFINITY;
     const float sink = p.sinks != nullptr ? p.sinks[head] * 1.4426950408889634f : -INFINITY;
-    m = sink;
-    for (int i = 0; i < n_src; ++i) {
-        const Source& s = src[i];
-        m = fmaxf(m, s.home_ml[s.row].x);
+    float m = sink;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll 4
-        for (int c = s.first; c < s.end; c += s.step) m = fmaxf(m, s.cont_ml[c * s.cont_tile + s.cont_row].x);
-    }
+        for (int c = 0; c < run[i].n; ++c) m = fmaxf(m, run[i].ml[c * run[i].ml_step].x);
     float l = sink == -INFINITY ? 0.0f : exp2f(sink - m);
-    float4 acc[4];
+    float acc[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float* part, int rows, int row, float2 ml) {
-        if (ml.x == -INFINITY) return;  // (nothing was stored)
-        const float a = exp2f(ml.x - m);
-        l = fmaf(ml.y, a, l);
+    for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 o = *reinterpret_cast<const float4*>(part + (static_cast<int64_t>(c4 + 4 * k) * rows + row) * 4);
-            acc[k].x = fmaf(o.x, a, acc[k].x);
-            acc[k].y = fmaf(o.y, a, acc[k].y);
-            acc[k].z = fmaf(o.z, a, acc[k].z);
-            acc[k].w = fmaf(o.w, a, acc[k].w);
+    for (int i = 0; i < 4; ++i) {
+        const Run& u = run[i];
+        for (int c0 = 0; c0 < u.n; c0 += 4) {
+            float a[4];
+            float4 o[4][2];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                a[c] = 0.0f;
+                o[c][0] = o[c][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c0 + c < u.n) {
+                    const float2 ml = u.ml[(c0 + c) * u.ml_step];
+                    if (ml.x != -INFINITY) {  // (else nothing was stored)
+                        a[c] = exp2f(ml.x - m);
+                        l = fmaf(ml.y, a[c], l);
+                        const float* part = u.part + (c0 + c) * u.part_step;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float* at = part + static_cast<int64_t>(c4 + 4 * k) * 4 * u.rows;
+                            if (i < 2 && quads) o[c][k] = *reinterpret_cast<const float4*>(at);
+                            else o[c][k] = make_float4(at[0], at[u.rows], at[2 * u.rows], at[3 * u.rows]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    acc[4 * k] = fmaf(o[c][k].x, a[c], acc[4 * k]);
+                    acc[4 * k + 1] = fmaf(o[c][k].y, a[c], acc[4 * k + 1]);
+                    acc[4 * k + 2] = fmaf(o[c][k].z, a[c], acc[4 * k + 2]);
+                    acc[4 * k + 3] = fmaf(o[c][k].w, a[c], acc[4 * k + 3]);
+                }
         }
-    };
-    for (int i = 0; i < n_src; ++i) {
-        const Source& s = src[i];
-        add(s.home, s.rows, s.row, s.home_ml[s.row]);
-#pragma unroll 2
-        for (int c = s.first; c < s.end; c += s.step)
-            add(s.cont + c * s.cont_tile * D, s.cont_rows, s.cont_row, s.cont_ml[c * s.cont_tile + s.cont_row]);
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     __nv_bfloat16* o = p.out + (t * p.Hq + head) * D;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint2*>(o + (c4 + 4 * k) * 4) = make_uint2(thd::pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
-                                                                    thd::pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<uint2*>(o + (c4 + 4 * k) * 4) =
+            make_uint2(thd::pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
+                       thd::pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
     if (p.lse != nullptr && blockIdx.y == 0 && lane < 8)
         p.lse[t * p.Hq + head] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
@@ -137,7 +176,7 @@ __global__ void __launch_bounds__(256) thd_sp_merge_kernel(const SpParams p) {
 constexpr int kMaxUnits = 4096;
 constexpr int kPagedCtas = 3 * thd::kSpLanes;  // three fit an SM
 // The paged kernel takes the prefix too when all rows of a kv head fit one row
-// tile of two 16-row groups.
+// tile of this many.
 constexpr int kPagedPrefixRows = 32;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -159,7 +198,7 @@ Layout make_layout(int n_req, int n_q, int Hq, int Hkv, int D) {
     y.rows = n_req * y.RB;
     const bool small = y.rows <= kPagedPrefixRows;
     const int want = small ? y.rows : y.RB;
-    y.pg_rows = want <= 16 ? 16 : want <= 32 || D == 256 ? 32 : 64;
+    y.pg_rows = want <= 8 ? 8 : want <= 16 ? 16 : want <= 32 || D == 256 ? 32 : 64;
     y.pg_units = (y.RB + y.pg_rows - 1) / y.pg_rows;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -168,12 +207,14 @@ Layout make_layout(int n_req, int n_q, int Hq, int Hkv, int D) {
         return here;
     };
     const size_t all = static_cast<size_t>(y.rows) * Hkv;
-    y.plan = take(8);
+    y.plan = take(sizeof(thd::SpPlan));
     y.own_home = take(all * D * 4);
     y.own_home_ml = take(all * 8);
     y.own_desc = take(static_cast<size_t>(n_req) * Hkv * y.pg_units * 8);
-    y.pg_cont = take(static_cast<size_t>(kPagedCtas) * y.pg_rows * D * 4);
-    y.pg_cont_ml = take(static_cast<size_t>(kPagedCtas) * y.pg_rows * 8);
+    // Workers of a CTA x rows of a tile: 32 rows (8 a warp) or 64.
+    const int warp_rows = y.pg_rows == 8 || D == 256 ? 8 : 16;
+    y.pg_cont = take(static_cast<size_t>(kPagedCtas) * 4 * warp_rows * D * 4);
+    y.pg_cont_ml = take(static_cast<size_t>(kPagedCtas) * 4 * warp_rows * 8);
     if (small) {
         y.pg_prefix = 1;
         y.pgp_home = take(static_cast<size_t>(Hkv) * y.pg_rows * D * 4);
@@ -213,6 +254,10 @@ bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
     if (done.load(std::memory_order_relaxed) >> dev & 1) return true;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    // All of the SM's shared memory, so that both kernels' CTAs fit it together.
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+        cudaSuccess)
+        return false;
     done.fetch_or(1ull << dev, std::memory_order_relaxed);
     return true;
 }
@@ -242,10 +287,10 @@ bool launch_prefix(const SpParams& p, const CUtensorMap& mk, const CUtensorMap& 
                         false, mk, mv, p, status);
 }
 
-template <int D, int WR>
+template <int D, int NR, int WR>
 bool launch_paged(const SpParams& p, const CUtensorMap& mk, const CUtensorMap& mv, int* status, bool early,
                   cudaStream_t stream) {
-    using C = thd::PagedConfig<D, WR>;
+    using C = thd::PagedConfig<D, NR, WR>;
     static std::atomic<uint64_t> done{0};
     return allow_smem(thd::thd_sp_paged_kernel<C>, C::SMEM_BYTES, done) &&
            launch_early(thd::thd_sp_paged_kernel<C>, dim3(p.pg_ctas), C::THREADS, C::SMEM_BYTES, stream, early, mk, mv, p,
@@ -267,20 +312,25 @@ int launch_all(SpParams p, const Maps& maps, bool any_keys, cudaStream_t stream)
             if (!launch_prefix<D>(p, maps.pre_k, maps.pre_v, st, stream)) return THD_ERR_CUDA;
             early = true;
         }
-        constexpr int KT = 32;  // (the least of the variants' tiles)
-        const int64_t own = (static_cast<int64_t>(p.max_blocks) * p.block + KT - 1) / KT * p.pg_units * p.n_req;
-        const int64_t pre = (static_cast<int64_t>(p.prefix_blocks) * p.block + KT - 1) / KT * p.pg_prefix;
-        p.pg_ctas = static_cast<int>(std::clamp<int64_t>((own + pre) * p.Hkv, 1, kPagedCtas));
+        // No more workers than there can be slices.
+        const int64_t slices = (static_cast<int64_t>(p.max_blocks) * p.pg_units * p.n_req +
+                                static_cast<int64_t>(p.prefix_blocks) * p.pg_prefix) * (p.block / 16) * p.Hkv;
+        p.pg_ctas = static_cast<int>(std::clamp<int64_t>(slices, 1, kPagedCtas));
         bool ok;
-        if (p.pg_rows == 16) ok = launch_paged<D, 1>(p, maps.pg_k, maps.pg_v, st, early, stream);
-        else if (p.pg_rows == 32) ok = launch_paged<D, 2>(p, maps.pg_k, maps.pg_v, st, early, stream);
-        else if constexpr (D != 256) ok = launch_paged<D, 4>(p, maps.pg_k, maps.pg_v, st, early, stream);
-        else ok = false;
+        const CUtensorMap &k = maps.pg_k, &v = maps.pg_v;
+        if (p.pg_rows == 8) ok = launch_paged<D, 1, 1>(p, k, v, st, early, stream);
+        else if constexpr (D == 256)
+            ok = p.pg_rows == 16 ? launch_paged<D, 1, 2>(p, k, v, st, early, stream)
+                                 : launch_paged<D, 1, 4>(p, k, v, st, early, stream);
+        else
+            ok = p.pg_rows == 16   ? launch_paged<D, 2, 1>(p, k, v, st, early, stream)
+                 : p.pg_rows == 32 ? launch_paged<D, 2, 2>(p, k, v, st, early, stream)
+                                   : launch_paged<D, 2, 4>(p, k, v, st, early, stream);
         if (!ok) return THD_ERR_CUDA;
         early = true;
     }
     const int64_t warps = static_cast<int64_t>(p.Hkv) * ((p.rows + 7) / 8);
-    if (!launch_early(thd_sp_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8), D / 64), 256, 0, stream, early, p))
+    if (!launch_early(thd_sp_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8), D / 32), 256, 0, stream, early, p))
         return THD_ERR_CUDA;
     return THD_OK;
 }
@@ -341,7 +391,7 @@ extern "C" int thd_attn_shared_prefix(const void* q, const void* k_cache, const 
     char* ws = static_cast<char*>(workspace);
     auto f = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
     auto f2 = [&](size_t at) { return reinterpret_cast<float2*>(ws + at); };
-    auto i2 = [&](size_t at) { return reinterpret_cast<int2*>(ws + at); };
+    auto i8 = [&](size_t at) { return reinterpret_cast<long long*>(ws + at); };
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.prefix_table = prefix ? prefix_table_or_null : nullptr;
     p.prefix_len = prefix ? prefix_len_or_null : nullptr;
@@ -373,22 +423,23 @@ extern "C" int thd_attn_shared_prefix(const void* q, const void* k_cache, const 
     p.pre_home_ml = f2(y.pre_home_ml);
     p.pre_cont = f(y.pre_cont);
     p.pre_cont_ml = f2(y.pre_cont_ml);
-    p.pre_plan = reinterpret_cast<int*>(ws + y.plan);
+    p.plan = reinterpret_cast<thd::SpPlan*>(ws + y.plan);
     p.pg_rows = y.pg_rows;
     p.pg_units = y.pg_units;
     p.pg_prefix = prefix ? y.pg_prefix : 0;
     p.own_home = f(y.own_home);
     p.own_home_ml = f2(y.own_home_ml);
-    p.own_desc = i2(y.own_desc);
+    p.own_desc = i8(y.own_desc);
     p.pgp_home = f(y.pgp_home);
     p.pgp_home_ml = f2(y.pgp_home_ml);
-    p.pgp_desc = i2(y.pgp_desc);
+    p.pgp_desc = i8(y.pgp_desc);
     p.pg_cont = f(y.pg_cont);
     p.pg_cont_ml = f2(y.pg_cont_ml);
     // Maps with the boxes of the prefix kernel (a page, 128 tokens at most) and
     // of the paged kernel (a page's part of a slice).
     Maps maps{};
-    const int slice = std::min(block_size, y.pg_rows == 16 ? 16 : 32);
+    p.pg_slice = D * (y.pg_rows == 8 || D == 256 ? 1 : 2) <= 128 ? 32 : 16;
+    const int slice = std::min(block_size, p.pg_slice);
     auto map = [&](CUtensorMap* m, const void* base, int box) {
         return thd::make_paged_map(m, base, num_blocks, block_size, Hkv, D, block_stride, token_stride, head_stride, box);
     };

@@ -14,9 +14,11 @@
 // tile, else to the CTA's own place (only a lane's first piece can begin inside
 // an item); the merge kernel adds them up in a fixed order.
 //
-// A partial tile is stored as [D / 4][rows][4] fp32 with (maximum, sum) per
-// row beside it: threads that hold neighbouring rows then write, and the merge
-// kernel reads, whole lines.
+// A partial tile is stored with the rows side by side, [D / 4][rows][4] fp32 by
+// the prefix kernel (a thread holds a row) and [D][rows] by the paged kernel (a
+// quad of threads holds 8 rows of a column), with (maximum, sum) per row beside
+// it, so that threads with neighbouring rows write whole sectors and the merge
+// kernel reads them.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -27,6 +29,13 @@
 namespace thd {
 
 constexpr int kSpLanes = 148;  // CTAs of the prefix kernel (one per SM)
+
+// What the kernels derived from the lengths, for the merge kernel.
+struct SpPlan {
+    long long pg_units;
+    int pg_lanes;
+    int pre_tiles;  // key tiles (paged kernel: slices) of the prefix
+};
 
 struct SpParams {
     const __nv_bfloat16* q;
@@ -51,20 +60,21 @@ struct SpParams {
     float2* pre_home_ml;
     float* pre_cont;
     float2* pre_cont_ml;
-    int* pre_plan;  // [2]: first key tile, number of key tiles
     // paged kernel
     int pg_rows;        // rows of its row tile
     int pg_units;       // row tiles of a request
     int pg_prefix;      // row tiles of the prefix that it takes (0: none)
     int pg_ctas;
+    int pg_slice;       // keys of a slice
     float* own_home;
     float2* own_home_ml;
-    int2* own_desc;     // first and last CTA of an item
+    long long* own_desc;  // first unit of an item
     float* pgp_home;
     float2* pgp_home_ml;
-    int2* pgp_desc;
+    long long* pgp_desc;
     float* pg_cont;
     float2* pg_cont_ml;
+    SpPlan* plan;
 };
 
 // First unit of lane l when `units` are cut into `lanes` ranges (lanes <= units,
@@ -100,10 +110,10 @@ __device__ __forceinline__ int sp_first_own(const SpParams& p, int n) {
     return p.window > 0 && t > p.window ? t - p.window : 0;
 }
 
-// Tiles of KT own keys that the queries of a request of n own tokens see.
-template <int KT>
-__device__ __forceinline__ int sp_own_tiles(const SpParams& p, int n) {
-    return n > 0 ? (n - 1) / KT + 1 - sp_first_own(p, n) / KT : 0;
+// Slices of KS own keys that the queries of a request of n own tokens see.
+template <int KS>
+__device__ __forceinline__ int sp_own_slices(const SpParams& p, int n) {
+    return n > 0 ? (n - 1) / KS + 1 - sp_first_own(p, n) / KS : 0;
 }
 
 }  // namespace thd

@@ -196,10 +196,7 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         const int lanes = static_cast<int>(min(units, static_cast<long long>(p.pre_lanes)));
         walk.x = my_lane < lanes ? lane_begin(units, lanes, my_lane) : 0;
         walk.x1 = my_lane < lanes ? lane_begin(units, lanes, my_lane + 1) : 0;
-        if (blockIdx.x == 0 && threadIdx.x == 0) {
-            p.pre_plan[0] = walk.first_tile;
-            p.pre_plan[1] = walk.n_tiles;
-        }
+        if (blockIdx.x == 0 && threadIdx.x == 0) p.plan->pre_tiles = walk.n_tiles;
     }
     PrefixPiece pc;
 
