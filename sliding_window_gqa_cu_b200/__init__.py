@@ -15,6 +15,7 @@ bf16 output ``[T, Hq, D]`` and fp32 log-sum-exp ``[T, Hq]``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -576,8 +577,8 @@ def thd_sparse_mla_get_error(stream=None) -> int:
 
 def _check_i32(name, t, shape, device):
     import torch
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
 
 
 def _check_cuda(name, t):
@@ -585,24 +586,42 @@ def _check_cuda(name, t):
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
-def _cache_strides(k_cache, v_cache, device):
-    """Checks a pair of paged caches [blocks, block_size, Hkv, D] and returns
-    (blocks, block_size, Hkv, D, block stride, token stride, head stride)."""
+def _allocate_on(stream, make):
+    """What ``make`` allocates, reused in the given stream's order (None: the current one)."""
     import torch
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4:
-            raise ValueError(f"{name} must be a bf16 tensor [blocks, block_size, kv_heads, head_dim] on {device}")
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-    nb, bs, Hkv, D = k_cache.shape
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _call_on(device, stream, entry, name, *args):
+    """Calls a C entry point on the device's given (None: current) stream.  A
+    serving step calls several a token, so this takes the short ways: the
+    device's guard only where another device is current."""
+    import torch
+    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = entry(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = entry(*args, handle)
+    if rc != 0:
+        raise ThdAttnError(rc, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _cache_layout(shape, k_strides, v_strides):
+    """The sizes and strides of a pair of caches of one shape, checked."""
+    nb, bs, Hkv, D = shape
     # the stride of a dimension of one element is never used: any value does
     dense = (bs * Hkv * D, Hkv * D, D)
 
     def strides(t):
-        return tuple(d if n <= 1 else s for n, s, d in zip(t.shape[:3], t.stride()[:3], dense))
-    if strides(k_cache) != strides(v_cache) or (D > 1 and (k_cache.stride(3) != 1 or v_cache.stride(3) != 1)):
+        return tuple(d if n <= 1 else s for n, s, d in zip(shape[:3], t[:3], dense))
+    if strides(k_strides) != strides(v_strides) or (D > 1 and (k_strides[3] != 1 or v_strides[3] != 1)):
         raise ValueError("k_cache and v_cache must have the same strides and a dense head_dim")
-    sb, st, sh = strides(k_cache)
+    sb, st, sh = strides(k_strides)
     # Distinct elements: sorted by stride, every dimension steps over the ones inside it.
     inside = D
     for s, n in sorted(((sb, nb), (st, bs), (sh, Hkv))):
@@ -611,6 +630,18 @@ def _cache_strides(k_cache, v_cache, device):
                 raise ValueError("the cache's blocks, tokens and heads must not overlap")
             inside = s * n
     return nb, bs, Hkv, D, sb, st, sh
+
+
+def _cache_strides(k_cache, v_cache, device):
+    """Checks a pair of paged caches [blocks, block_size, Hkv, D] and returns
+    (blocks, block_size, Hkv, D, block stride, token stride, head stride)."""
+    import torch
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype is not torch.bfloat16 or t.device != device or t.dim() != 4:
+            raise ValueError(f"{name} must be a bf16 tensor [blocks, block_size, kv_heads, head_dim] on {device}")
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    return _cache_layout(k_cache.shape, k_cache.stride(), v_cache.stride())
 
 
 def thd_kv_block_tables(seq_lens, new_lens, block_tables, free_blocks, free_count, block_size: int,
@@ -628,8 +659,6 @@ def thd_kv_block_tables(seq_lens, new_lens, block_tables, free_blocks, free_coun
     refused [1])``; each may be passed in (``seq_lens_out`` may be ``seq_lens``
     and ``free_count_out`` may be ``free_count``).
     """
-    import torch
-
     lib = load_library()
     _check_cuda("seq_lens", seq_lens)
     dev = seq_lens.device
@@ -637,33 +666,41 @@ def thd_kv_block_tables(seq_lens, new_lens, block_tables, free_blocks, free_coun
     if block_tables.dim() != 2 or free_blocks.dim() != 1 or n_rows < 0:
         raise ValueError("block_tables must be [requests, max_blocks], free_blocks [capacity], n_rows >= 0")
     M = block_tables.shape[1]
-    for name, t, shape in (("seq_lens", seq_lens, (B,)), ("new_lens", new_lens, (B,)),
-                           ("block_tables", block_tables, (B, M)),
-                           ("free_blocks", free_blocks, tuple(free_blocks.shape)),
-                           ("free_count", free_count, (1,))):
-        _check_i32(name, t, shape, dev)
+    _check_i32("seq_lens", seq_lens, (B,), dev)
+    _check_i32("new_lens", new_lens, (B,), dev)
+    _check_i32("block_tables", block_tables, (B, M), dev)
+    _check_i32("free_blocks", free_blocks, free_blocks.shape, dev)
+    _check_i32("free_count", free_count, (1,), dev)
     if first_position is not None:
         _check_i32("first_position", first_position, (1,), dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    outs = []
-    with torch.cuda.stream(stream):
-        for name, t, shape in (("seq_lens_out", seq_lens_out, (B,)), ("free_count_out", free_count_out, (1,)),
-                               ("cu_new", cu_new, (B + 1,)), ("slots", slots, (n_rows,)),
-                               ("positions", positions, (n_rows,)), ("refused", refused, (1,))):
-            if t is None:
-                t = torch.empty(shape, dtype=torch.int32, device=dev)
-            _check_i32(name, t, shape, dev)
-            outs.append(t)
-    with torch.cuda.device(dev):
-        rc = lib.thd_kv_block_tables(
-            seq_lens.data_ptr(), new_lens.data_ptr(), B, int(block_size), block_tables.data_ptr(), M,
-            free_blocks.data_ptr(), free_blocks.numel(), free_count.data_ptr(),
-            first_position.data_ptr() if first_position is not None else None, n_rows,
-            *(t.data_ptr() for t in outs), ctypes.c_void_p(stream.cuda_stream))
-    if rc != 0:
-        raise ThdAttnError(rc, "thd_kv_block_tables")
-    return tuple(outs)
+    outs = (slots, positions, seq_lens_out, cu_new, free_count_out, refused)
+    sizes = (n_rows, n_rows, B, B + 1, 1, 1)
+    if any(t is not None for t in outs):
+        for name, t, n in zip(("slots", "positions", "seq_lens_out", "cu_new", "free_count_out", "refused"), outs, sizes):
+            if t is not None:
+                _check_i32(name, t, (n,), dev)
+    # What the caller does not pass in comes from one allocation; slots and
+    # positions on 16-byte borders.
+    want = [(i, n) for i, (t, n) in enumerate(zip(outs, sizes)) if t is None]
+    if want:
+        pad = -n_rows % 4
+        parts = [n for i, n in want]
+        at = list(range(len(parts)))
+        if pad and want[0][0] < 2:
+            parts.insert(1, pad)
+            at = [0] + [i + 1 for i in at[1:]]
+        views = _allocate_on(stream, lambda: seq_lens.new_empty((sum(parts),))).split_with_sizes(parts)
+        outs = list(outs)
+        for (i, _), j in zip(want, at):
+            outs[i] = views[j]
+    slots, positions, seq_lens_out, cu_new, free_count_out, refused = outs
+    _call_on(dev, stream, lib.thd_kv_block_tables, "thd_kv_block_tables",
+             seq_lens.data_ptr(), new_lens.data_ptr(), B, int(block_size), block_tables.data_ptr(), M,
+             free_blocks.data_ptr(), free_blocks.shape[0], free_count.data_ptr(),
+             first_position.data_ptr() if first_position is not None else None, n_rows,
+             seq_lens_out.data_ptr(), free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
+             positions.data_ptr(), refused.data_ptr())
+    return seq_lens_out, free_count_out, cu_new, slots, positions, refused
 
 
 def thd_kv_write(k, v, slots, k_cache, v_cache, stream=None):
@@ -681,21 +718,16 @@ def thd_kv_write(k, v, slots, k_cache, v_cache, stream=None):
     _check_cuda("k", k)
     dev = k.device
     nb, bs, Hkv, D, sb, st, sh = _cache_strides(k_cache, v_cache, dev)
-    T = k.shape[0]
+    T, shape = k.shape[0], (k.shape[0], Hkv, D)
+    rows = []
     for name, t in (("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16 or t.device != dev or tuple(t.shape) != (T, Hkv, D) or \
-                (T > 0 and not t[0].is_contiguous()):
+        if t.dtype is not torch.bfloat16 or t.device != dev or t.shape != shape or \
+                (T > 0 and ((Hkv > 1 and t.stride(1) != D) or t.stride(2) != 1)):
             raise ValueError(f"{name} must be a bf16 tensor [rows, {Hkv}, {D}] on {dev} with dense heads")
+        rows.append(t.stride(0) if T > 1 else Hkv * D)
     _check_i32("slots", slots, (T,), dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev):
-        rc = lib.thd_kv_write(
-            k.data_ptr(), v.data_ptr(), k.stride(0) if T > 1 else Hkv * D, v.stride(0) if T > 1 else Hkv * D,
-            slots.data_ptr(), T, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, sb, st, sh,
-            ctypes.c_void_p(stream.cuda_stream))
-    if rc != 0:
-        raise ThdAttnError(rc, "thd_kv_write")
+    _call_on(dev, stream, lib.thd_kv_write, "thd_kv_write", k.data_ptr(), v.data_ptr(), rows[0], rows[1],
+             slots.data_ptr(), T, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, sb, st, sh)
     return k_cache, v_cache
 
 
@@ -721,7 +753,7 @@ def thd_attn_shared_prefix(q, k_cache, v_cache, block_tables, kv_lens, prefix_ta
     lib = load_library()
     _check_cuda("q", q)
     dev = q.device
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+    if q.dtype is not torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 CUDA tensor [requests * n_q, heads, head_dim]")
     nb, bs, Hkv, D, sb, st, sh = _cache_strides(k_cache, v_cache, dev)
     T, Hq = q.shape[0], q.shape[1]
@@ -745,35 +777,30 @@ def thd_attn_shared_prefix(q, k_cache, v_cache, block_tables, kv_lens, prefix_ta
     if scale is None:
         scale = D ** -0.5
     if sinks is not None:
-        if sinks.dtype != torch.float32 or sinks.device != dev or sinks.numel() != Hq or not sinks.is_contiguous():
+        if sinks.dtype is not torch.float32 or sinks.device != dev or sinks.numel() != Hq or not sinks.is_contiguous():
             raise ValueError("sinks must be a contiguous fp32 CUDA tensor of Hq values")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    need = int(lib.thd_attn_shared_prefix_workspace_bytes(B, n_q, Hq, Hkv, D))
-    with torch.cuda.stream(stream):   # what is allocated here is reused in this stream's order
-        if out is None:
-            out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-        if return_lse and lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
-    for name, t, dt, shape in (("out", out, torch.bfloat16, (T, Hq, D)), ("lse", lse, torch.float32, (T, Hq))):
-        if t is not None and (t.dtype != dt or t.device != dev or not t.is_contiguous() or tuple(t.shape) != shape):
-            raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape} on {dev}")
-    if workspace.device != dev or not workspace.is_contiguous():
+    if out is None:
+        out = _allocate_on(stream, lambda: q.new_empty((T, Hq, D)))
+    elif out.dtype is not torch.bfloat16 or out.device != dev or out.shape != (T, Hq, D) or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous bf16 tensor of shape {(T, Hq, D)} on {dev}")
+    if lse is None:
+        if return_lse:
+            lse = _allocate_on(stream, lambda: q.new_empty((T, Hq), dtype=torch.float32))
+    elif lse.dtype is not torch.float32 or lse.device != dev or lse.shape != (T, Hq) or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(T, Hq)} on {dev}")
+    if workspace is None:
+        need = int(lib.thd_attn_shared_prefix_workspace_bytes(B, n_q, Hq, Hkv, D))
+        workspace = _allocate_on(stream, lambda: q.new_empty((max(need, 16),), dtype=torch.uint8))
+    elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    with torch.cuda.device(dev):
-        rc = lib.thd_attn_shared_prefix(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, sb, st, sh,
-            prefix_table.data_ptr() if prefix_table is not None else None,
-            prefix_table.numel() if prefix_table is not None else 0,
-            prefix_len.data_ptr() if prefix_len is not None else None,
-            block_tables.data_ptr(), M, kv_lens.data_ptr(), B, n_q, Hq, Hkv, D, int(window), float(scale),
-            sinks.data_ptr() if sinks is not None else None, out.data_ptr(),
-            lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), ctypes.c_void_p(stream.cuda_stream))
-    if rc != 0:
-        raise ThdAttnError(rc, "thd_attn_shared_prefix")
+    _call_on(dev, stream, lib.thd_attn_shared_prefix, "thd_attn_shared_prefix",
+             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, sb, st, sh,
+             prefix_table.data_ptr() if prefix_table is not None else None,
+             prefix_table.numel() if prefix_table is not None else 0,
+             prefix_len.data_ptr() if prefix_len is not None else None,
+             block_tables.data_ptr(), M, kv_lens.data_ptr(), B, n_q, Hq, Hkv, D, int(window), float(scale),
+             sinks.data_ptr() if sinks is not None else None, out.data_ptr(),
+             lse.data_ptr() if lse is not None else None, workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
 

@@ -5,22 +5,29 @@
 // Block tables.  With n, m the cached and new tokens of a request and bs the
 // page size: held = ceil(n / bs) pages are in its table, a growing request
 // needs ceil((n + m) / bs) - held more, an ended one gives its held back.
-// Three prefix sums over the requests say everything: cu (rows), back (pages
-// given back) and off (pages wanted).  Then every output is a flat loop whose
-// element finds its request by bisection:
+// Prefix sums over the requests say everything: cu (rows), back (pages given
+// back) and off (pages wanted).  Then every output is a flat loop whose element
+// finds its request by bisection:
 //   pushed page y:  free[n_free + y]       = table[b][y - back[b]]
-//   popped page x:  table[b][held + x - off[b]] = free[top - 1 - x]
+//   popped page x:  table[b][held + x - off[b]] = stack(top - 1 - x)
 //   packed row t:   pos = n + t - cu[b], page = pos / bs; a page below held is
 //                   in the table, another one is popped page
-//                   off[b] + page - held, read from the stack itself so that
-//                   rows need not wait for the table.
-// Latency bound: a few KB to a MB move.
+//                   off[b] + page - held
+// where stack(i) is free[i] below n_free and pushed page i - n_free above, read
+// from the ended request's own row.  So no output depends on another one, and
+// only the lengths (which may be updated in place) must be read before anything
+// is written: CTAs that share the work need one barrier between the two, which a
+// cluster has.  Each of them computes the sums for itself.
+//
+// Latency bound: a few KB to a MB move.  A step of 256 requests is one CTA, whose
+// time is loads, three barriers and the stores one after the other.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "../../include/thd_attn.h"
+#include "sm100_ptx.cuh"
 #include "tma_map.h"
 
 namespace {
@@ -28,6 +35,9 @@ namespace {
 constexpr int kTabThreads = 1024;
 constexpr int kMaxReq = 8192;  // four int32 arrays of the requests in shared memory
 constexpr int32_t kRefused = static_cast<int32_t>(0x80000000u);  // flag on a refused request's length
+// CTAs that share the rows of a larger step, and from how many rows on.
+constexpr int kTabCluster = 8;
+constexpr int64_t kTabClusterRows = 2048;
 
 struct TabParams {
     const int32_t* seq_lens;
@@ -46,8 +56,9 @@ struct TabParams {
     int n_req, block, max_blocks;
 };
 
-// Exclusive prefix sum of one value per thread over the block, and the total.
-__device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
+// Exclusive prefix sums of one value per thread over the block, and the total.
+// `sums` (32 values) is used by one call only, so one barrier is enough.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t x = v;
 #pragma unroll
@@ -55,36 +66,17 @@ __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
+    if (lane == 31) sums[warp] = x;
     __syncthreads();
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int64_t s = warp_sums[lane];
+    int64_t s = sums[lane];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        warp_sums[lane] = s;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
     }
-    __syncthreads();
-    total = warp_sums[31];
-    return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
-}
-
-// Largest value over the block (values >= 0).
-__device__ int64_t block_max(int64_t v, int64_t* warp_vals) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const int64_t y = __shfl_xor_sync(0xffffffffu, v, o);
-        v = y > v ? y : v;
-    }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) warp_vals[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0;
-    for (int w = 0; w < kTabThreads / 32; ++w) v = warp_vals[w] > v ? warp_vals[w] : v;
-    return v;
+    total = __shfl_sync(0xffffffffu, s, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
+    return x - v + (warp > 0 ? before : 0);
 }
 
 // Last b in [0, n) with a[b] <= x (a is non-decreasing and a[0] <= x).
@@ -97,119 +89,173 @@ __device__ __forceinline__ int find_request(const int32_t* a, int n, int32_t x) 
     return lo;
 }
 
+// PER consecutive requests per thread.
+template <int PER>
 __global__ void __launch_bounds__(kTabThreads) thd_kv_block_tables_kernel(const TabParams p) {
     extern __shared__ int32_t arrays[];
     int32_t* cu = arrays;               // first packed row
     int32_t* back = cu + p.n_req;       // first pushed page
     int32_t* off = back + p.n_req;      // first popped page
     int32_t* seq = off + p.n_req;       // cached tokens
-    __shared__ int64_t warp_sums[32];
+    __shared__ int64_t sums[4][32];
     const int tid = threadIdx.x;
-    const int per = (p.n_req + kTabThreads - 1) / kTabThreads;  // consecutive requests of a thread
-    const int b0 = min(p.n_req, tid * per), b1 = min(p.n_req, b0 + per);
     const int64_t bs = p.block;
-    const int n_free = static_cast<int>(min(static_cast<int64_t>(max(*p.free_count, 0)), p.capacity));
+    const int ctas = gridDim.x, me = blockIdx.x;
+    constexpr int64_t kMax = 0x7fffffff;
 
+    int n[PER], m[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int b = tid * PER + i;
+        n[i] = b < p.n_req ? p.seq_lens[b] : -1;
+        m[i] = b < p.n_req ? p.new_lens[b] : 0;
+    }
+    const int n_free = static_cast<int>(min(static_cast<int64_t>(max(*p.free_count, 0)), p.capacity));
+    const int first = p.first_pos != nullptr ? *p.first_pos : 0;
+    auto pages = [&](int64_t tokens) { return (tokens + bs - 1) / bs; };
+    int64_t held[PER], total[PER];  // pages of n and of n + m tokens
     int64_t add = 0, give = 0;
-    for (int b = b0; b < b1; ++b) {
-        const int n = p.seq_lens[b], m = p.new_lens[b];
-        if (n >= 0 && m >= 0) add += m;
-        if (n >= 0 && m < 0) give += min((n + bs - 1) / bs, static_cast<int64_t>(p.max_blocks));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        held[i] = n[i] > 0 ? (n[i] - 1) / p.block + 1 : 0;
+        total[i] = held[i];
+        if (n[i] >= 0 && m[i] > 0) {
+            add += m[i];
+            total[i] = pages(static_cast<int64_t>(n[i]) + m[i]);
+        }
+        if (n[i] >= 0 && m[i] < 0) give += min(held[i], static_cast<int64_t>(p.max_blocks));
     }
     int64_t rows, pushed;
-    add = block_scan(add, warp_sums, rows);
-    give = block_scan(give, warp_sums, pushed);
+    add = block_scan(add, sums[0], rows);
+    give = block_scan(give, sums[1], pushed);
     const int64_t top = min(n_free + pushed, p.capacity);
-    constexpr int64_t kMax = 0x7fffffff;
     // Pages wanted; a request refused for its width or rows wants none.
     int64_t want = 0;
+    uint32_t narrow = 0;
     {
         int64_t r = add, g = give;
-        for (int b = b0; b < b1; ++b) {
-            const int n = p.seq_lens[b], m = p.new_lens[b];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int b = tid * PER + i;
+            if (b >= p.n_req) break;
             cu[b] = static_cast<int32_t>(min(r, kMax));
             back[b] = static_cast<int32_t>(min(g, kMax));
-            seq[b] = n;
-            if (n >= 0 && m >= 0) {
-                r += m;
-                const int64_t total = (static_cast<int64_t>(n) + m + bs - 1) / bs;
-                if (m > 0 && total <= p.max_blocks && r <= p.n_rows) want += total - (n + bs - 1) / bs;
-            } else if (n >= 0) {
-                g += min((n + bs - 1) / bs, static_cast<int64_t>(p.max_blocks));
+            if (n[i] >= 0 && m[i] >= 0) {
+                r += m[i];
+                if (m[i] > 0 && (total[i] > p.max_blocks || r > p.n_rows)) narrow |= 1u << i;
+                else want += total[i] - held[i];
+            } else if (n[i] >= 0) {
+                g += min(held[i], static_cast<int64_t>(p.max_blocks));
             }
         }
     }
     int64_t wanted;
-    int64_t o = block_scan(want, warp_sums, wanted);
-    int64_t taken = 0;
+    int64_t o = block_scan(want, sums[2], wanted);
+    int taken = 0;  // (at most the capacity)
     int n_refused = 0;
-    {
-        int64_t r = add;
-        for (int b = b0; b < b1; ++b) {
-            const int n = p.seq_lens[b], m = p.new_lens[b];
-            off[b] = static_cast<int32_t>(min(o, kMax));
-            if (n < 0 || m <= 0) continue;
-            r += m;
-            const int64_t total = (static_cast<int64_t>(n) + m + bs - 1) / bs;
-            bool no = total > p.max_blocks || r > p.n_rows;
-            if (!no) {
-                const int64_t need = total - (n + bs - 1) / bs;
-                no = need > 0 && o + need > top;
-                if (!no && need > 0) taken = o + need;
-                o += need;
-            }
-            if (no) {
-                ++n_refused;
-                seq[b] = n | kRefused;
-            }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int b = tid * PER + i;
+        if (b >= p.n_req) break;
+        off[b] = static_cast<int32_t>(min(o, kMax));
+        bool no = (narrow >> i & 1u) != 0;
+        if (!no && n[i] >= 0 && m[i] > 0) {
+            const int64_t need = total[i] - held[i];
+            no = need > 0 && o + need > top;
+            if (!no && need > 0) taken = static_cast<int>(o + need);
+            o += need;
         }
+        n_refused += no;
+        seq[b] = no ? n[i] | kRefused : n[i];
+        m[i] = no ? 0 : m[i];
     }
-    int64_t all_refused;
-    block_scan(n_refused, warp_sums, all_refused);
-    taken = block_max(taken, warp_sums);
-
-    // Pages of ended requests onto the stack (a page below max_blocks of a
-    // row, so the row's own entries).
-    const int64_t n_push = min(pushed, p.capacity - n_free);
-    for (int64_t y = tid; y < n_push; y += kTabThreads) {
-        const int b = find_request(back, p.n_req, static_cast<int32_t>(y));
-        p.free_blocks[n_free + y] = p.table[static_cast<int64_t>(b) * p.max_blocks + (y - back[b])];
-    }
+    taken = __reduce_max_sync(0xffffffffu, taken);
+    n_refused = __reduce_add_sync(0xffffffffu, n_refused);
+    if ((tid & 31) == 0) sums[3][tid >> 5] = static_cast<int64_t>(n_refused) << 32 | static_cast<uint32_t>(taken);
+    // Every CTA has read the lengths and the count; its arrays are complete.
     __syncthreads();
+    if (ctas > 1) thd::cluster_sync();
+    {
+        const int64_t v = sums[3][tid & 31];
+        taken = __reduce_max_sync(0xffffffffu, static_cast<int>(v & 0xffffffff));
+        n_refused = __reduce_add_sync(0xffffffffu, static_cast<int>(v >> 32));
+    }
 
-    if (tid == 0) {
-        *p.free_out = static_cast<int32_t>(top - taken);
-        *p.refused = static_cast<int32_t>(all_refused);
-        p.cu_out[p.n_req] = static_cast<int32_t>(min(rows, kMax));
+    // The page at stack place i.
+    auto stack = [&](int64_t i) -> int32_t {
+        if (i < n_free) return p.free_blocks[i];
+        const int32_t y = static_cast<int32_t>(i - n_free);
+        const int b = find_request(back, p.n_req, y);
+        return p.table[static_cast<int64_t>(b) * p.max_blocks + (y - back[b])];
+    };
+    if (me == 0) {
+        if (tid == 0) {
+            *p.free_out = static_cast<int32_t>(top - taken);
+            *p.refused = n_refused;
+            p.cu_out[p.n_req] = static_cast<int32_t>(min(rows, kMax));
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int b = tid * PER + i;
+            if (b >= p.n_req) break;
+            p.cu_out[b] = cu[b];
+            p.seq_out[b] = n[i] < 0 || m[i] < 0 ? -1 : n[i] + m[i];
+        }
     }
-    for (int b = b0; b < b1; ++b) {
-        const int n = p.seq_lens[b], m = p.new_lens[b];
-        p.cu_out[b] = cu[b];
-        p.seq_out[b] = n < 0 || m < 0 ? -1 : (m > 0 && seq[b] < 0) ? n : n + m;
-    }
-    for (int64_t x = tid; x < taken; x += kTabThreads) {
+    const int64_t at = static_cast<int64_t>(me) * kTabThreads + tid, step = static_cast<int64_t>(ctas) * kTabThreads;
+    // Pages of ended requests onto the stack (below max_blocks of a row, so the
+    // row's own entries).
+    const int64_t n_push = min(pushed, p.capacity - n_free);
+    for (int64_t y = at; y < n_push; y += step) p.free_blocks[n_free + y] = stack(n_free + y);
+    // New pages into the tables.
+    for (int64_t x = at; x < taken; x += step) {
         const int b = find_request(off, p.n_req, static_cast<int32_t>(x));
-        const int64_t held = (seq[b] + bs - 1) / bs;
-        p.table[static_cast<int64_t>(b) * p.max_blocks + held + (x - off[b])] = p.free_blocks[top - 1 - x];
+        const int held_b = seq[b] > 0 ? (seq[b] - 1) / p.block + 1 : 0;
+        p.table[static_cast<int64_t>(b) * p.max_blocks + held_b + (x - off[b])] = stack(top - 1 - x);
     }
-    const int first = p.first_pos != nullptr ? *p.first_pos : 0;
-    for (int64_t t = tid; t < p.n_rows; t += kTabThreads) {
-        int slot = -1, position = 0;
-        if (t < rows) {
-            const int b = find_request(cu, p.n_req, static_cast<int32_t>(t));
-            const int n = seq[b] & ~kRefused;
-            const int64_t far = static_cast<int64_t>(n) + (t - cu[b]);  // (a refused request may pass 2^31)
-            position = static_cast<int>(min(first + far, kMax));
+    // Four packed rows at a time: the first one's request by bisection, the
+    // others' by walking on.
+    const bool vec = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15u) == 0;
+    for (int64_t t0 = at * 4; t0 < p.n_rows; t0 += step * 4) {
+        int slot[4], position[4];
+        int b = t0 < rows ? find_request(cu, p.n_req, static_cast<int32_t>(t0)) : 0;
+        int last_page = -1;
+        int32_t id = -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t t = t0 + i;
+            slot[i] = -1;
+            position[i] = 0;
+            if (t >= rows) continue;
+            while (b + 1 < p.n_req && cu[b + 1] <= t) {
+                ++b;
+                last_page = -1;
+            }
+            const int have = seq[b] & ~kRefused;
+            const int64_t far = static_cast<int64_t>(have) + (t - cu[b]);  // (a refused request may pass 2^31)
+            position[i] = static_cast<int>(min(first + far, kMax));
             if (seq[b] >= 0) {
-                const int at = static_cast<int>(far);
-                const int held = static_cast<int>((n + bs - 1) / bs), page = at / p.block;
-                const int32_t id = page < held ? p.table[static_cast<int64_t>(b) * p.max_blocks + page]
-                                               : p.free_blocks[top - 1 - (off[b] + page - held)];
-                if (id >= 0 && id < kMax / bs) slot = id * p.block + at % p.block;
+                const int pos = static_cast<int>(far), page = pos / p.block;
+                if (page != last_page) {
+                    const int held_b = have > 0 ? (have - 1) / p.block + 1 : 0;
+                    id = page < held_b ? p.table[static_cast<int64_t>(b) * p.max_blocks + page]
+                                       : stack(top - 1 - (off[b] + page - held_b));
+                    last_page = page;
+                }
+                if (id >= 0 && id < kMax / bs) slot[i] = id * p.block + (pos - page * p.block);
             }
         }
-        p.slots[t] = slot;
-        p.positions[t] = position;
+        if (vec && t0 + 3 < p.n_rows) {
+            *reinterpret_cast<int4*>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4*>(p.positions + t0) = make_int4(position[0], position[1], position[2], position[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (t0 + i < p.n_rows) {
+                    p.slots[t0 + i] = slot[i];
+                    p.positions[t0 + i] = position[i];
+                }
+        }
     }
 }
 
@@ -240,6 +286,26 @@ __global__ void __launch_bounds__(256) thd_kv_write_kernel(const WriteParams p) 
     }
 }
 
+template <int PER>
+int launch_tables(const TabParams& p, int ctas, cudaStream_t stream) {
+    const int smem = 16 * p.n_req;
+    if (smem > 40000 && cudaFuncSetAttribute(thd_kv_block_tables_kernel<PER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             16 * kMaxReq) != cudaSuccess)
+        return THD_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kTabThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ctas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, thd_kv_block_tables_kernel<PER>, p) == cudaSuccess ? THD_OK : THD_ERR_CUDA;
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
@@ -268,13 +334,13 @@ extern "C" int thd_kv_block_tables(const int32_t* seq_lens, const int32_t* new_l
     TabParams p{seq_lens, new_lens, block_tables, free_blocks, free_count, first_position_or_null,
                 seq_lens_out, free_count_out, cu_new, slots, positions, refused,
                 free_capacity, n_rows, n_req, block_size, max_blocks};
-    const int smem = 16 * n_req;
-    if (smem > 40000 &&
-        cudaFuncSetAttribute(thd_kv_block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             16 * kMaxReq) != cudaSuccess)
-        return THD_ERR_CUDA;
-    thd_kv_block_tables_kernel<<<1, kTabThreads, smem, static_cast<cudaStream_t>(stream_ptr)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? THD_OK : THD_ERR_CUDA;
+    const int ctas = n_rows > kTabClusterRows ? kTabCluster : 1;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    const int per = (n_req + kTabThreads - 1) / kTabThreads;
+    if (per == 1) return launch_tables<1>(p, ctas, stream);
+    if (per == 2) return launch_tables<2>(p, ctas, stream);
+    if (per <= 4) return launch_tables<4>(p, ctas, stream);
+    return launch_tables<8>(p, ctas, stream);
 }
 
 extern "C" int thd_kv_write(const void* k, const void* v, int64_t k_row_stride, int64_t v_row_stride,
