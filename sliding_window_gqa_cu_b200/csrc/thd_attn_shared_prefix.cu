@@ -19,6 +19,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <numeric>
 #include <type_traits>
 
 #include "../../include/thd_attn.h"
@@ -35,140 +36,143 @@ using thd::SpParams;
 __device__ int g_sp_status;
 
 // Adds up the parts of every row in a fixed order.  A warp takes 8 consecutive
-// rows of a kv head x 32 columns; a thread one row and two groups of four
-// columns.  The parts are a few MB in L2; a row that many CTAs worked on has
-// many of them, so four are loaded at a time.
+// rows of a kv head x 16 columns, a thread four columns of a row, eight parts at
+// a time: the parts are a few MB in L2 and the kernel is bound by the latency of
+// its loads (plan, then places, then parts), so all that can be are issued
+// together.
 template <int D>
 __global__ void __launch_bounds__(256) thd_sp_merge_kernel(const SpParams p) {
     constexpr int NT = thd::PrefixConfig<D>::NT;
+    constexpr int BATCH = 8;
     const int lane = threadIdx.x & 31;
     const int groups = (p.rows + 7) / 8;
     const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int h = static_cast<int>(w / groups);
     const int r = static_cast<int>(w - static_cast<int64_t>(h) * groups) * 8 + (lane & 7);
-    const int c4 = blockIdx.y * 8 + (lane >> 3);
+    const int c4 = blockIdx.y * 4 + (lane >> 3);
+    const bool here = h < p.Hkv && r < p.rows;
+    const int b = here ? r / p.RB : 0, rr = r - b * p.RB;
+    const int g = r % p.G, head = h * p.G + g;
+    const int64_t t = r / p.G;
+    const int64_t bh = static_cast<int64_t>(b) * p.Hkv + h;
+    const bool quads = p.pre_lanes > 0;  // the prefix's parts are the prefix kernel's
+    const int pre_item = r / p.pg_rows * p.Hkv + h;
+    const int64_t own_item = bh * p.pg_units + rr / p.pg_rows;
     thd::wait_for_previous_grid();
-    if (h >= p.Hkv || r >= p.rows) return;
-    const int b = r / p.RB, rr = r - b * p.RB;
+    if (!here) return;
     const int n = thd::sp_own_len(p, b);
+    const float sink = p.sinks != nullptr ? p.sinks[head] * 1.4426950408889634f : -INFINITY;
+    thd::SpPlan plan{0, 0, 0};
+    long long own_begin = 0, pre_begin = 0;
+    if (p.any_keys) {
+        plan = *p.plan;
+        own_begin = p.own_desc[own_item];  // (means nothing for an item without keys)
+        if (p.pg_prefix > 0) pre_begin = p.pgp_desc[pre_item];
+        if (!quads && p.pg_prefix == 0) plan.pre_tiles = 0;
+    }
     if (n < 0) return;
 
-    // Runs of parts: the home place and the own places of the following
-    // workers, of the prefix and of the request's pages.
+    // Runs of parts, of the prefix and of the request's pages: the home place,
+    // then the own places of the following workers.
     struct Run {
-        const float* part;   // of this thread's row
-        const float2* ml;
+        const float* home;   // of this thread's row and columns
+        const float2* home_ml;
+        const float* cont;
+        const float2* cont_ml;
         int64_t part_step, ml_step;
-        int n, rows;
-    } run[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) run[i].n = 0;
-    const int pre_tiles = p.pre_lanes > 0 || p.pg_prefix > 0 ? p.plan->pre_tiles : 0;
-    // Parts of the item whose keys begin at unit x, `count` units of keys, in
-    // `units` units over `lanes` workers, `step` CTAs to a worker.
-    auto runs = [&](Run& home, Run& cont, long long units, int lanes, long long x, int count, int step, int member,
-                    int tile_rows, int tile_row) {
+        int n, home_rows, cont_rows;
+    } run[2];
+    run[0].n = run[1].n = 0;
+    // The item whose `count` units of keys begin at unit x of `units`, which are
+    // cut over `lanes` workers of `step` CTAs each.
+    auto workers = [&](Run& u, long long units, int lanes, long long x, int count, int step, int member, int tile_rows) {
         const int first = thd::lane_of(units, lanes, x), last = thd::lane_of(units, lanes, x + count - 1);
-        home.n = 1;
-        home.part_step = home.ml_step = 0;
-        cont.n = last - first;
-        cont.rows = tile_rows;
-        const int64_t at = (static_cast<int64_t>(first + 1) * step + member) * tile_rows;
-        cont.part += at * D;
-        cont.ml += at + tile_row;
-        cont.part_step = static_cast<int64_t>(step) * tile_rows * D;
-        cont.ml_step = static_cast<int64_t>(step) * tile_rows;
+        u.n = last - first + 1;
+        u.part_step = static_cast<int64_t>(step) * tile_rows * D;
+        u.ml_step = static_cast<int64_t>(step) * tile_rows;
+        // (places of workers first + 1, .. follow: part 0 is the home place)
+        const int64_t at = (static_cast<int64_t>(first) * step + member) * tile_rows;
+        u.cont += at * D;
+        u.cont_ml += at;
     };
-    const bool quads = p.pre_lanes > 0;  // the prefix's parts are [D / 4][rows][4]
-    if (pre_tiles > 0 && quads) {
-        const int tile = r >> 7, group = tile / NT, q = tile - group * NT;
-        const long long units = static_cast<long long>((p.pre_groups + p.pre_width - 1) / p.pre_width) * p.Hkv * pre_tiles;
+    if (plan.pre_tiles > 0 && quads) {
+        const int tile = r >> 7, group = tile / NT, q = tile - group * NT, row = r & 127;
+        const long long units = static_cast<long long>((p.pre_groups + p.pre_width - 1) / p.pre_width) * p.Hkv * plan.pre_tiles;
         const int lanes = static_cast<int>(min(units, static_cast<long long>(p.pre_lanes)));
         const int64_t at = (static_cast<int64_t>(h) * p.pre_groups + group) * NT + q;
-        run[0].part = p.pre_home + at * (128 * D) + (r & 127) * 4;
-        run[0].ml = p.pre_home_ml + at * 128 + (r & 127);
-        run[0].rows = 128;
-        run[1].part = p.pre_cont + (r & 127) * 4 + static_cast<int64_t>(q) * (128 * D);
-        run[1].ml = p.pre_cont_ml + q * 128;
-        runs(run[0], run[1], units, lanes, (static_cast<long long>(group / p.pre_width) * p.Hkv + h) * pre_tiles, pre_tiles,
-             p.pre_width, group % p.pre_width, NT * 128, r & 127);
-        run[1].rows = 128;
-    } else if (pre_tiles > 0) {
-        const int item = r / p.pg_rows * p.Hkv + h, row = r % p.pg_rows;
-        run[0].part = p.pgp_home + static_cast<int64_t>(item) * p.pg_rows * D + row;
-        run[0].ml = p.pgp_home_ml + static_cast<int64_t>(item) * p.pg_rows + row;
-        run[0].rows = p.pg_rows;
-        run[1].part = p.pg_cont + row;
-        run[1].ml = p.pg_cont_ml;
-        runs(run[0], run[1], p.plan->pg_units, p.plan->pg_lanes, p.pgp_desc[item] + thd::kItemUnits, pre_tiles, 1, 0,
-             p.pg_rows, row);
+        run[0].home = p.pre_home + at * (128 * D) + (c4 * 128 + row) * 4;
+        run[0].home_ml = p.pre_home_ml + at * 128 + row;
+        run[0].cont = p.pre_cont + static_cast<int64_t>(q) * (128 * D) + (c4 * 128 + row) * 4;
+        run[0].cont_ml = p.pre_cont_ml + q * 128 + row;
+        workers(run[0], units, lanes, (static_cast<long long>(group / p.pre_width) * p.Hkv + h) * plan.pre_tiles,
+                plan.pre_tiles, p.pre_width, group % p.pre_width, NT * 128);
+    } else if (plan.pre_tiles > 0) {
+        const int row = r % p.pg_rows;
+        run[0].home_rows = run[0].cont_rows = p.pg_rows;
+        run[0].home = p.pgp_home + static_cast<int64_t>(pre_item) * p.pg_rows * D + c4 * 4 * p.pg_rows + row;
+        run[0].home_ml = p.pgp_home_ml + static_cast<int64_t>(pre_item) * p.pg_rows + row;
+        run[0].cont = p.pg_cont + c4 * 4 * p.pg_rows + row;
+        run[0].cont_ml = p.pg_cont_ml + row;
+        workers(run[0], plan.pg_units, plan.pg_lanes, pre_begin + thd::kItemUnits, plan.pre_tiles, 1, 0, p.pg_rows);
     }
     const int own = p.pg_slice == 32 ? thd::sp_own_slices<32>(p, n) : thd::sp_own_slices<16>(p, n);
     if (own > 0) {
-        const int64_t bh = static_cast<int64_t>(b) * p.Hkv + h;
-        run[2].part = p.own_home + bh * p.RB * D + rr;
-        run[2].ml = p.own_home_ml + bh * p.RB + rr;
-        run[2].rows = p.RB;
-        run[3].part = p.pg_cont + rr % p.pg_rows;
-        run[3].ml = p.pg_cont_ml;
-        runs(run[2], run[3], p.plan->pg_units, p.plan->pg_lanes,
-             p.own_desc[bh * p.pg_units + rr / p.pg_rows] + thd::kItemUnits, own, 1, 0, p.pg_rows, rr % p.pg_rows);
+        const int row = rr % p.pg_rows;
+        run[1].home_rows = p.RB;
+        run[1].cont_rows = p.pg_rows;
+        run[1].home = p.own_home + bh * p.RB * D + static_cast<int64_t>(c4) * 4 * p.RB + rr;
+        run[1].home_ml = p.own_home_ml + bh * p.RB + rr;
+        run[1].cont = p.pg_cont + c4 * 4 * p.pg_rows + row;
+        run[1].cont_ml = p.pg_cont_ml + row;
+        workers(run[1], plan.pg_units, plan.pg_lanes, own_begin + thd::kItemUnits, own, 1, 0, p.pg_rows);
     }
-    const int g = r % p.G, head = h * p.G + g;
-    const int64_t t = r / p.G;
-    const float sink = p.sinks != nullptr ? p.sinks[head] * 1.4426950408889634f : -INFINITY;
-    float m = sink;
+    float m = sink, l = sink == -INFINITY ? 0.0f : 1.0f;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll 4
-        for (int c = 0; c < run[i].n; ++c) m = fmaxf(m, run[i].ml[c * run[i].ml_step].x);
-    float l = sink == -INFINITY ? 0.0f : exp2f(sink - m);
-    float acc[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const Run& u = run[i];
-        for (int c0 = 0; c0 < u.n; c0 += 4) {
-            float a[4];
-            float4 o[4][2];
+#pragma unroll 1
+        for (int c0 = 0; c0 < u.n; c0 += BATCH) {
+            float2 ml[BATCH];
+            float4 o[BATCH];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                a[c] = 0.0f;
-                o[c][0] = o[c][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c0 + c < u.n) {
-                    const float2 ml = u.ml[(c0 + c) * u.ml_step];
-                    if (ml.x != -INFINITY) {  // (else nothing was stored)
-                        a[c] = exp2f(ml.x - m);
-                        l = fmaf(ml.y, a[c], l);
-                        const float* part = u.part + (c0 + c) * u.part_step;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float* at = part + static_cast<int64_t>(c4 + 4 * k) * 4 * u.rows;
-                            if (i < 2 && quads) o[c][k] = *reinterpret_cast<const float4*>(at);
-                            else o[c][k] = make_float4(at[0], at[u.rows], at[2 * u.rows], at[3 * u.rows]);
-                        }
-                    }
+            for (int c = 0; c < BATCH; ++c) {
+                const int k = min(c0 + c, u.n - 1);
+                const float* at = k == 0 ? u.home : u.cont + k * u.part_step;
+                ml[c] = k == 0 ? *u.home_ml : u.cont_ml[k * u.ml_step];
+                if (i == 0 && quads) {
+                    o[c] = *reinterpret_cast<const float4*>(at);
+                } else {
+                    const int rows = k == 0 ? u.home_rows : u.cont_rows;
+                    o[c] = make_float4(at[0], at[rows], at[2 * static_cast<int64_t>(rows)], at[3 * static_cast<int64_t>(rows)]);
                 }
             }
+            float top = m;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < BATCH; ++c) {
+                if (c0 + c >= u.n) ml[c].x = -INFINITY;
+                top = fmaxf(top, ml[c].x);
+            }
+            const float a = m == -INFINITY ? 0.0f : exp2f(m - top);
+            m = top;
+            l *= a;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    acc[4 * k] = fmaf(o[c][k].x, a[c], acc[4 * k]);
-                    acc[4 * k + 1] = fmaf(o[c][k].y, a[c], acc[4 * k + 1]);
-                    acc[4 * k + 2] = fmaf(o[c][k].z, a[c], acc[4 * k + 2]);
-                    acc[4 * k + 3] = fmaf(o[c][k].w, a[c], acc[4 * k + 3]);
-                }
+            for (int k = 0; k < 4; ++k) acc[k] *= a;
+#pragma unroll
+            for (int c = 0; c < BATCH; ++c) {
+                if (ml[c].x == -INFINITY) continue;  // (its part may never have been written)
+                const float x = exp2f(ml[c].x - top);
+                l = fmaf(ml[c].y, x, l);
+                acc[0] = fmaf(o[c].x, x, acc[0]);
+                acc[1] = fmaf(o[c].y, x, acc[1]);
+                acc[2] = fmaf(o[c].z, x, acc[2]);
+                acc[3] = fmaf(o[c].w, x, acc[3]);
+            }
         }
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    __nv_bfloat16* o = p.out + (t * p.Hq + head) * D;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        *reinterpret_cast<uint2*>(o + (c4 + 4 * k) * 4) =
-            make_uint2(thd::pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
-                       thd::pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+    *reinterpret_cast<uint2*>(p.out + (t * p.Hq + head) * D + c4 * 4) =
+        make_uint2(thd::pack_bf16x2(acc[0] * inv, acc[1] * inv), thd::pack_bf16x2(acc[2] * inv, acc[3] * inv));
     if (p.lse != nullptr && blockIdx.y == 0 && lane < 8)
         p.lse[t * p.Hq + head] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
@@ -288,49 +292,46 @@ bool launch_prefix(const SpParams& p, const CUtensorMap& mk, const CUtensorMap& 
 }
 
 template <int D, int NR, int WR>
-bool launch_paged(const SpParams& p, const CUtensorMap& mk, const CUtensorMap& mv, int* status, bool early,
-                  cudaStream_t stream) {
+bool launch_paged(const SpParams& p, int* status, bool early, cudaStream_t stream) {
     using C = thd::PagedConfig<D, NR, WR>;
     static std::atomic<uint64_t> done{0};
     return allow_smem(thd::thd_sp_paged_kernel<C>, C::SMEM_BYTES, done) &&
-           launch_early(thd::thd_sp_paged_kernel<C>, dim3(p.pg_ctas), C::THREADS, C::SMEM_BYTES, stream, early, mk, mv, p,
-                        status);
+           launch_early(thd::thd_sp_paged_kernel<C>, dim3(p.pg_ctas), C::THREADS, C::SMEM_BYTES, stream, early, p, status);
 }
 
 struct Maps {
-    CUtensorMap pre_k, pre_v, pg_k, pg_v;
+    CUtensorMap k, v;
 };
 
 template <int D>
-int launch_all(SpParams p, const Maps& maps, bool any_keys, cudaStream_t stream) {
+int launch_all(SpParams p, const Maps& maps, cudaStream_t stream) {
     void* status = nullptr;
     if (cudaGetSymbolAddress(&status, g_sp_status) != cudaSuccess) return THD_ERR_CUDA;
     int* st = static_cast<int*>(status);
     bool early = false;
-    if (any_keys) {
+    if (p.any_keys) {
         if (p.pre_lanes > 0) {
-            if (!launch_prefix<D>(p, maps.pre_k, maps.pre_v, st, stream)) return THD_ERR_CUDA;
+            if (!launch_prefix<D>(p, maps.k, maps.v, st, stream)) return THD_ERR_CUDA;
             early = true;
         }
-        // No more workers than there can be slices.
+        // No more CTAs than there can be slices (tables may be longer than what is used).
         const int64_t slices = (static_cast<int64_t>(p.max_blocks) * p.pg_units * p.n_req +
                                 static_cast<int64_t>(p.prefix_blocks) * p.pg_prefix) * (p.block / 16) * p.Hkv;
         p.pg_ctas = static_cast<int>(std::clamp<int64_t>(slices, 1, kPagedCtas));
         bool ok;
-        const CUtensorMap &k = maps.pg_k, &v = maps.pg_v;
-        if (p.pg_rows == 8) ok = launch_paged<D, 1, 1>(p, k, v, st, early, stream);
+        if (p.pg_rows == 8) ok = launch_paged<D, 1, 1>(p, st, early, stream);
         else if constexpr (D == 256)
-            ok = p.pg_rows == 16 ? launch_paged<D, 1, 2>(p, k, v, st, early, stream)
-                                 : launch_paged<D, 1, 4>(p, k, v, st, early, stream);
+            ok = p.pg_rows == 16 ? launch_paged<D, 1, 2>(p, st, early, stream)
+                                 : launch_paged<D, 1, 4>(p, st, early, stream);
         else
-            ok = p.pg_rows == 16   ? launch_paged<D, 2, 1>(p, k, v, st, early, stream)
-                 : p.pg_rows == 32 ? launch_paged<D, 2, 2>(p, k, v, st, early, stream)
-                                   : launch_paged<D, 2, 4>(p, k, v, st, early, stream);
+            ok = p.pg_rows == 16   ? launch_paged<D, 2, 1>(p, st, early, stream)
+                 : p.pg_rows == 32 ? launch_paged<D, 2, 2>(p, st, early, stream)
+                                   : launch_paged<D, 2, 4>(p, st, early, stream);
         if (!ok) return THD_ERR_CUDA;
         early = true;
     }
     const int64_t warps = static_cast<int64_t>(p.Hkv) * ((p.rows + 7) / 8);
-    if (!launch_early(thd_sp_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8), D / 32), 256, 0, stream, early, p))
+    if (!launch_early(thd_sp_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8), D / 16), 256, 0, stream, early, p))
         return THD_ERR_CUDA;
     return THD_OK;
 }
@@ -393,6 +394,12 @@ extern "C" int thd_attn_shared_prefix(const void* q, const void* k_cache, const 
     auto f2 = [&](size_t at) { return reinterpret_cast<float2*>(ws + at); };
     auto i8 = [&](size_t at) { return reinterpret_cast<long long*>(ws + at); };
     p.q = static_cast<const __nv_bfloat16*>(q);
+    p.kc = static_cast<const __nv_bfloat16*>(k_cache);
+    p.vc = static_cast<const __nv_bfloat16*>(v_cache);
+    p.block_stride = block_stride;
+    p.token_stride = token_stride;
+    p.head_stride = head_stride;
+    p.any_keys = any_keys ? 1 : 0;
     p.prefix_table = prefix ? prefix_table_or_null : nullptr;
     p.prefix_len = prefix ? prefix_len_or_null : nullptr;
     p.tables = block_tables;
@@ -435,24 +442,26 @@ extern "C" int thd_attn_shared_prefix(const void* q, const void* k_cache, const 
     p.pgp_desc = i8(y.pgp_desc);
     p.pg_cont = f(y.pg_cont);
     p.pg_cont_ml = f2(y.pg_cont_ml);
-    // Maps with the boxes of the prefix kernel (a page, 128 tokens at most) and
-    // of the paged kernel (a page's part of a slice).
-    Maps maps{};
     p.pg_slice = D * (y.pg_rows == 8 || D == 256 ? 1 : 2) <= 128 ? 32 : 16;
-    const int slice = std::min(block_size, p.pg_slice);
-    auto map = [&](CUtensorMap* m, const void* base, int box) {
-        return thd::make_paged_map(m, base, num_blocks, block_size, Hkv, D, block_stride, token_stride, head_stride, box);
-    };
-    if (any_keys && (!map(&maps.pg_k, k_cache, slice) || !map(&maps.pg_v, v_cache, slice)))
-        return THD_ERR_INVALID_ARG;
-    if (any_keys && p.pre_lanes > 0 &&
-        (!map(&maps.pre_k, k_cache, p.box_rows) || !map(&maps.pre_v, v_cache, p.box_rows)))
-        return THD_ERR_INVALID_ARG;
+    Maps maps{};
+    if (any_keys && p.pre_lanes > 0) {
+        const int64_t bs = num_blocks > 1 ? block_stride : 0, hs = Hkv > 1 ? head_stride : 0;
+        const int64_t g = std::max<int64_t>(std::gcd(bs, hs), 8);
+        const int64_t places = (num_blocks - 1) * (bs / g) + (Hkv - 1) * (hs / g) + 1;
+        if (places > kMax) return THD_ERR_UNSUPPORTED;
+        p.places = static_cast<int>(places);
+        p.place_block = static_cast<int>(bs / g);
+        p.place_head = static_cast<int>(hs / g);
+        auto map = [&](CUtensorMap* m, const void* base) {
+            return thd::make_paged_map(m, base, block_size, D, token_stride, g, places, p.box_rows, std::min(D, 128) / 64);
+        };
+        if (!map(&maps.k, k_cache) || !map(&maps.v, v_cache)) return THD_ERR_INVALID_ARG;
+    }
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     switch (D) {
-        case 64: return launch_all<64>(p, maps, any_keys, stream);
-        case 128: return launch_all<128>(p, maps, any_keys, stream);
-        default: return launch_all<256>(p, maps, any_keys, stream);
+        case 64: return launch_all<64>(p, maps, stream);
+        case 128: return launch_all<128>(p, maps, stream);
+        default: return launch_all<256>(p, maps, stream);
     }
 }
 

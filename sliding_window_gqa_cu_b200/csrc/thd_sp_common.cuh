@@ -39,6 +39,9 @@ struct SpPlan {
 
 struct SpParams {
     const __nv_bfloat16* q;
+    const __nv_bfloat16* kc;
+    const __nv_bfloat16* vc;
+    int64_t block_stride, token_stride, head_stride;  // of the caches, in elements
     const int32_t* prefix_table;
     const int32_t* prefix_len;
     const int32_t* tables;
@@ -49,9 +52,11 @@ struct SpParams {
     int num_blocks, block, block_shift, prefix_blocks, max_blocks;
     int n_req, n_q, Hq, Hkv, G, window;
     float scale_log2;
+    int any_keys;  // there are blocks and tables
     int RB;        // rows of a request and kv head
     int rows;      // rows of a kv head
     int box_rows;  // tokens of one TMA box of the prefix kernel
+    int places, place_block, place_head;  // extent and steps of its map's place coordinate
     // prefix kernel
     int pre_groups;  // row groups of a kv head
     int pre_width;   // CTAs of a lane (row groups in step)
@@ -77,15 +82,20 @@ struct SpParams {
     SpPlan* plan;
 };
 
+// (32-bit division where it is enough: the 64-bit one takes some 100 instructions.)
 // First unit of lane l when `units` are cut into `lanes` ranges (lanes <= units,
 // so that none is empty).
 __device__ __forceinline__ long long lane_begin(long long units, int lanes, int l) {
-    return units * l / lanes;
+    const unsigned long long at = static_cast<unsigned long long>(units) * l;
+    if (at >> 32 == 0) return static_cast<unsigned>(at) / static_cast<unsigned>(lanes);
+    return static_cast<long long>(at / static_cast<unsigned>(lanes));
 }
 
 // The lane that holds unit x: the largest l with units * l / lanes < x + 1.
 __device__ __forceinline__ int lane_of(long long units, int lanes, long long x) {
-    return static_cast<int>(((x + 1) * lanes - 1) / units);
+    const unsigned long long at = static_cast<unsigned long long>(x + 1) * lanes - 1;
+    if (at >> 32 == 0) return static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(units));
+    return static_cast<int>(at / static_cast<unsigned long long>(units));
 }
 
 __device__ __forceinline__ int sp_prefix_len(const SpParams& p) {

@@ -10,10 +10,11 @@
 // high, 1/16 of it used, and send the scores through TMEM.)
 //
 // A worker is WR warps of 8 NR rows each, which share a ring of slots (a K or V
-// slice of KS keys each); its first warp issues the TMA loads, the next slice
-// into a slot as soon as the slot has been read.  Workers never wait for each
-// other.  16 KB a warp, 64 KB a CTA are in flight: three CTAs on an SM, or one
-// beside the prefix kernel.
+// slice of KS keys each) and refill a slot as soon as it has been read.  Workers
+// never wait for each other.  16 KB a warp, 64 KB a CTA are in flight: three
+// CTAs on an SM, or one beside the prefix kernel.  The loads are cp.async: a page
+// of 16 tokens is too small a box for TMA, which took 75 to 85 ns per box and SM
+// here (24 to 27 GB/s of the SM's share of 44).
 //
 // Work split: (request, kv head, row tile) items; a unit is a slice, and an item
 // counts kItemUnits more for its start and end.  The units of the batch are cut
@@ -36,6 +37,16 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
+// 16 bytes into shared memory, zeros if !there.
+__device__ __forceinline__ void load16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// Arrives on the barrier when this thread's loads so far have landed.
+__device__ __forceinline__ void loads_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // Transposes the 8 x 8 matrix of 16-bit elements that the warp holds.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
@@ -54,6 +65,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 
 // What starting and ending an item costs, in units.
 constexpr int kItemUnits = 1;
+// Units that a worker gets at least: fewer would make more parts to add up than
+// they save (a part costs the merge kernel about as much as a slice takes here).
+constexpr int kWorkerUnits = 4;
 
 template <int D_, int NR_, int WR_>
 struct PagedConfig {
@@ -63,7 +77,7 @@ struct PagedConfig {
     static constexpr int WORKERS = 4 / WR;              // of a CTA
     static constexpr int ROWS = 8 * NR * WR;            // rows of a row tile
     static constexpr int KS = D * NR <= 128 ? 32 : 16;  // keys of a slice (what the registers hold)
-    static constexpr int CHUNK_BYTES = KS * 128;
+    static constexpr int ROW_BYTES = D * 2;
     static constexpr int SLOT_BYTES = KS * D * 2;
     static constexpr int NSLOT = 16384 * WR / SLOT_BYTES;
     static constexpr int THREADS = 128;
@@ -74,8 +88,7 @@ struct PagedConfig {
     static constexpr int SMEM_BAR = 65536;
     static constexpr int B_FULL = 0, B_EMPTY = WORKERS * NSLOT, NUM_BARS = 2 * WORKERS * NSLOT;
     static constexpr int SMEM_START = SMEM_BAR + NUM_BARS * 8;  // int64 [16]
-    static constexpr int SMEM_MASK = SMEM_START + 128;          // uint32 [WORKERS][NSLOT]: 16-key parts in pages of the cache
-    static constexpr int SMEM_ABORT = SMEM_MASK + WORKERS * NSLOT * 4;
+    static constexpr int SMEM_ABORT = SMEM_START + 128;
     static constexpr int SMEM_BYTES = SMEM_ABORT + 4;
     static_assert(NSLOT >= 2, "K and V of a slice");
 };
@@ -107,7 +120,8 @@ struct PagedWalk {
             long long* desc;
             int at, slices;
             if (x < pre_units) {
-                const int item = static_cast<int>(x / (pre_slices + kItemUnits));
+                const int item = static_cast<int>(x <= 0x7fffffff ? static_cast<int>(x) / (pre_slices + kItemUnits)
+                                                                   : x / (pre_slices + kItemUnits));
                 item_begin = static_cast<long long>(item) * (pre_slices + kItemUnits);
                 at = static_cast<int>(x - item_begin);
                 slices = pre_slices;
@@ -191,8 +205,7 @@ struct PagedWalk {
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::RESIDENT)
-thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                    const SpParams p, int* status) {
+thd_sp_paged_kernel(const SpParams p, int* status) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
     const int warp = threadIdx.x >> 5;
@@ -203,18 +216,11 @@ thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::SMEM_ABORT);
 
     if (threadIdx.x == 0) {
-        tma_prefetch_desc(&tmap_k);
-        tma_prefetch_desc(&tmap_v);
         for (int s = 0; s < C::WORKERS * C::NSLOT; ++s) {
-            mbar_init(bar(C::B_FULL + s), 1);
+            mbar_init(bar(C::B_FULL + s), 32 * C::WR);
             mbar_init(bar(C::B_EMPTY + s), C::WR);
         }
-        int bad = *reinterpret_cast<volatile int*>(status) != 0 ? 1 : 0;
-        if ((sbase & 1023u) != 0) {  // the swizzled tiles need it
-            atomicCAS(status, 0, kStatusBadItem);
-            bad = 1;
-        }
-        *abort_flag = bad;
+        *abort_flag = *reinterpret_cast<volatile int*>(status) != 0 ? 1 : 0;
         fence_barrier_init();
     }
 
@@ -262,7 +268,8 @@ thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         walk.pre_units = walk.pre_slices > 0
                              ? static_cast<long long>(p.pg_prefix) * p.Hkv * (walk.pre_slices + kItemUnits) : 0;
         const long long units = walk.pre_units + total;
-        const int lanes = static_cast<int>(min(units, static_cast<long long>(p.pg_ctas) * C::WORKERS));
+        const int lanes = static_cast<int>(min((units + kWorkerUnits - 1) / kWorkerUnits,
+                                               static_cast<long long>(p.pg_ctas) * C::WORKERS));
         // Where each worker's range begins among the own units.
 #pragma unroll
         for (int i = 0; i < C::WORKERS; ++i) {
@@ -298,14 +305,12 @@ thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 
     {
         const int wr = warp % C::WR, wk = warp / C::WR;
-        const bool leader = wr == 0;  // issues the worker's loads
         const int mi = lane >> 3, m8 = lane & 7;
         const int r8 = lane >> 2, c2 = (lane & 3) * 2;
         const float sl2 = p.scale_log2;
         constexpr float kTau = 8.0f;  // rescale only when a maximum grows by more than 2^8
         const uint32_t ring = sbase + wk * (C::NSLOT * C::SLOT_BYTES);
         const int full0 = C::B_FULL + wk * C::NSLOT, empty0 = C::B_EMPTY + wk * C::NSLOT;
-        volatile uint32_t* const masks = reinterpret_cast<volatile uint32_t*>(smem + C::SMEM_MASK) + wk * C::NSLOT;
         int pos = 0, issued = 0;  // ring positions read and loaded
         bool ok = *abort_flag == 0;
         PagedPiece pc;
@@ -315,8 +320,10 @@ thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
             const int end_pos = pos + 2 * pc.n;
             int slice = 0;             // of the next load
             int page0 = 0, page1 = 0;  // thread t: pages of slice (slice & ~31) + t, first and second 16 keys
+            uint32_t there = 0;        // bit 2 (issued slices) + part: its page exists (the last 16 slices)
+            const int64_t head = static_cast<int64_t>(pc.h) * p.head_stride + (lane % (C::D / 8)) * 8;
             auto load_next = [&]() {
-                if (!leader || issued >= end_pos) return;
+                if (issued >= end_pos) return;
                 const int slot = issued % C::NSLOT;
                 const bool v = ((issued ^ pos0) & 1) != 0;
                 if (C::WR > 1 && issued >= C::NSLOT) {
@@ -324,11 +331,11 @@ thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                     if (!ok) return;
                 }
                 if (!v && (slice & 31) == 0) {
-                    auto page_of = [&](int k) -> int {  // one past the cache if there is none
+                    auto page_of = [&](int k) -> int {  // -1 if there is none
                         const int idx = k >> p.block_shift;
                         int id = -1;
                         if (slice + lane < pc.n && idx < pc.table_len) id = pc.table[idx];
-                        return id >= 0 && id < p.num_blocks ? id : p.num_blocks;
+                        return id < p.num_blocks ? id : -1;
                     };
                     const int key = (pc.slice + slice + lane) * C::KS;
                     page0 = page_of(key);
@@ -336,19 +343,30 @@ thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                 }
                 const int id0 = __shfl_sync(0xffffffffu, page0, slice & 31);
                 const int id1 = C::KS == 32 ? __shfl_sync(0xffffffffu, page1, slice & 31) : id0;
-                if (lane == 0) {
-                    const int row = ((pc.slice + slice) * C::KS) & (p.block - 1);
-                    masks[slot] = (id0 < p.num_blocks ? 1u : 0u) | (id1 < p.num_blocks ? 2u : 0u);
-                    mbar_arrive_expect_tx(bar(full0 + slot), C::SLOT_BYTES);
-                    const uint32_t dst = ring + slot * C::SLOT_BYTES;
-                    const CUtensorMap* map = v ? &tmap_v : &tmap_k;
+                // A warp loads its share of the slice's rows, 16 bytes a thread.
+                constexpr int LANES = C::D / 8;               // threads of a row
+                constexpr int STEP = 32 / LANES * C::WR;      // rows of the worker at a time
+                const int row = lane / LANES + wr * (32 / LANES);
+                const int in_page = (((pc.slice + slice) * C::KS) & (p.block - 1)) + row;
+                const __nv_bfloat16* cache = v ? p.vc : p.kc;
+                const uint32_t dst = ring + slot * C::SLOT_BYTES + row * C::ROW_BYTES;
+                const int64_t step = static_cast<int64_t>(STEP) * p.token_stride;
 #pragma unroll
-                    for (int c = 0; c < C::D / 64; ++c) {
-                        tma_load_4d(dst + c * C::CHUNK_BYTES, map, bar(full0 + slot), c * 64, pc.h, row, id0);
-                        if (C::KS == 32 && p.block == 16)
-                            tma_load_4d(dst + c * C::CHUNK_BYTES + 2048, map, bar(full0 + slot), c * 64, pc.h, row, id1);
+                for (int part = 0; part < C::KS / 16; ++part) {
+                    const int id = part == 0 ? id0 : id1;
+                    const __nv_bfloat16* src = cache;
+                    if (id >= 0)
+                        src += static_cast<int64_t>(id) * p.block_stride +
+                               static_cast<int64_t>(in_page + (part == 1 && p.block != 16 ? 16 : 0)) * p.token_stride + head;
+#pragma unroll
+                    for (int i = 0; i < 16 / STEP; ++i) {
+                        const int rr = part * 16 + i * STEP;  // + row: the row in the slice
+                        load16(dst + rr * C::ROW_BYTES + (((lane % LANES) ^ ((rr + row) & 7)) << 4), src + (id >= 0 ? i * step : 0),
+                               id >= 0);
                     }
                 }
+                loads_arrive(bar(full0 + slot));
+                if (!v) there = there << 2 | (id0 >= 0 ? 1u : 0u) | (id1 >= 0 ? 2u : 0u);
                 ++issued;
                 if (v) ++slice;
             };
@@ -418,7 +436,8 @@ thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                 uint32_t pf[C::KS / 16][C::NR][2];
                 bool edge = false;
                 if (rows_here) {
-                    const uint32_t parts = masks[ks];  // 16-key parts whose page exists
+                    // 16-key parts whose page exists
+                    const uint32_t parts = there >> (2 * ((issued - pos - 1) >> 1)) & 3u;
                     float s[C::KS / 16][C::NR][4];
 #pragma unroll
                     for (int i = 0; i < C::KS / 16; ++i)
@@ -426,13 +445,13 @@ thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                         for (int t = 0; t < C::NR; ++t)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) s[i][t][e] = 0.0f;
-                    const uint32_t ka = ring + ks * C::SLOT_BYTES + ((mi & 1) * 8 + m8) * 128;
+                    const uint32_t ka = ring + ks * C::SLOT_BYTES + ((mi & 1) * 8 + m8) * C::ROW_BYTES;
 #pragma unroll
                     for (int kk = 0; kk < C::D / 16; ++kk)
 #pragma unroll
                         for (int i = 0; i < C::KS / 16; ++i) {
                             uint32_t a[4];
-                            ldsm4(ka + (kk >> 2) * C::CHUNK_BYTES + i * 16 * 128 + ((((kk & 3) * 2 + (mi >> 1)) ^ m8) << 4), a);
+                            ldsm4(ka + i * 16 * C::ROW_BYTES + (((kk * 2 + (mi >> 1)) ^ m8) << 4), a);
 #pragma unroll
                             for (int t = 0; t < C::NR; ++t) mma16816(s[i][t], a, qf[t][kk][0], qf[t][kk][1]);
                         }
@@ -509,7 +528,7 @@ thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                 ok = warp_wait(bar(full0 + vs), (pos / C::NSLOT) & 1, abort_flag, status);
                 if (!ok) break;
                 if (rows_here) {
-                    const uint32_t va = ring + vs * C::SLOT_BYTES + ((mi >> 1) * 8 + m8) * 128;
+                    const uint32_t va = ring + vs * C::SLOT_BYTES + ((mi >> 1) * 8 + m8) * C::ROW_BYTES;
                     auto pv = [&](auto masked) {
 #pragma unroll
                         for (int i = 0; i < C::KS / 16; ++i) {
@@ -524,8 +543,7 @@ thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
 #pragma unroll
                             for (int d = 0; d < C::D / 16; ++d) {
                                 uint32_t a[4];
-                                ldsm4_trans(va + (d >> 2) * C::CHUNK_BYTES + i * 16 * 128 +
-                                                ((((d & 3) * 2 + (mi & 1)) ^ m8) << 4), a);
+                                ldsm4_trans(va + i * 16 * C::ROW_BYTES + (((d * 2 + (mi & 1)) ^ m8) << 4), a);
                                 if (masked) {
                                     a[0] &= keep0;
                                     a[1] &= keep0;
@@ -567,8 +585,7 @@ thd_sp_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                 }
         }
         // After an abort let the loads in flight land before the CTA ends.
-        if (!ok && leader && lane == 0)
-            for (int i = pos; i < issued; ++i) drain_wait(bar(full0 + i % C::NSLOT), (i / C::NSLOT) & 1);
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
 
     __syncthreads();

@@ -15,7 +15,11 @@
 // first), and the sequence (bundle of groups, kv head, key tile) is cut into
 // equal ranges, one per lane of CTAs.
 //
-// Warps: 4 NT softmax warps (thread = row), a TMA producer, an MMA issuer.
+// Warps: 4 NT softmax warps (thread = row), a TMA producer for K and one for V, an
+// MMA issuer.  A TMA instruction takes about 50 ns whatever its size, so one box
+// holds a page's tokens (128 at most) x all columns of a slot: [tokens / 8]
+// [column chunk][8 tokens][64 columns], whose groups of 8 tokens have one stride
+// over the pages of a tile, as the matrix descriptors need it.
 // The kernel leaves registers and, at D <= 128, shared memory for a CTA of the
 // paged kernel on the same SM: that one is bound by memory.  For that a
 // thread holds half a row of scores at a time; the first half is read from TMEM
@@ -37,13 +41,15 @@ struct PrefixConfig {
     static constexpr int SUB = D / SC;            // slots of a K or V tile
     static constexpr int CH = SC / 64;            // 128-byte chunks of a slot row
     static constexpr int NSLOT = D == 64 ? 6 : D == 128 ? 3 : 4;
-    static constexpr int BOX_BYTES = BN * 128;    // one chunk of a slot
+    static constexpr int Q_CHUNK_BYTES = 128 * 128;    // one chunk of a Q tile
+    static constexpr int GROUP_BYTES = CH * 1024;      // 8 keys of a slot, chunk by chunk
     static constexpr int SLOT_BYTES = BN * SC * 2;
     static constexpr int Q_TILE_BYTES = 128 * D * 2;
     static constexpr int SOFTMAX_WARPS = 4 * NT;
-    static constexpr int PRODUCER_WARP = SOFTMAX_WARPS;
-    static constexpr int MMA_WARP = SOFTMAX_WARPS + 1;
-    static constexpr int THREADS = (SOFTMAX_WARPS + 2) * 32;
+    static constexpr int K_WARP = SOFTMAX_WARPS;
+    static constexpr int V_WARP = SOFTMAX_WARPS + 1;
+    static constexpr int MMA_WARP = SOFTMAX_WARPS + 2;
+    static constexpr int THREADS = (SOFTMAX_WARPS + 3) * 32;
     // Threads that the register budget is made for: 128 registers a thread leave
     // a quarter of the registers to a CTA of the paged kernel.
     static constexpr int BOUND = D == 256 ? 384 : 512;
@@ -200,73 +206,61 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
     }
     PrefixPiece pc;
 
-    if (warp == C::PRODUCER_WARP) {
-        // ------------------------------------------------------ TMA producer
+    if (warp == C::K_WARP || warp == C::V_WARP) {
+        // ----------------------------------------------- TMA producers (K, V)
         if (!skip) {
-            if (lane == 0) {
-                tma_prefetch_desc(&tmap_k);
-                tma_prefetch_desc(&tmap_v);
-            }
-            const int boxes = C::BN / p.box_rows;  // boxes of a chunk, one lane each
+            const bool is_v = warp == C::V_WARP;
+            const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
+            if (lane == 0) tma_prefetch_desc(map);
+            const int boxes = C::BN / p.box_rows;  // of a slot, one lane each
             const int box = lane < boxes ? lane : 0;
-            int pos = 0, issued = 0;
+            int pos = 0;        // ring position
+            uint32_t mine = 0;  // bit i: this warp loaded position pos - 1 - i
             bool ok = true;
-            // Page of this lane's box of key tile kt (one past the cache if there is none).
-            auto page_of = [&](int kt) -> int {
+            // Place of this lane's box of key tile kt (behind the cache if it has no page).
+            auto place_of = [&](int kt, int h) -> int {
                 const int idx = (kt * C::BN + box * p.box_rows) >> p.block_shift;
                 int id = -1;
                 if (idx < p.prefix_blocks) id = p.prefix_table[idx];
-                return id >= 0 && id < p.num_blocks ? id : p.num_blocks;
-            };
-            auto load_tile = [&](const CUtensorMap* map, int kt, int id, int h) {
-                const int row = (kt * C::BN + box * p.box_rows) & (p.block - 1);
-                for (int s = 0; s < C::SUB && ok; ++s) {
-                    const int slot = pos % C::NSLOT;
-                    ok = warp_wait(bar(C::B_SLOT_EMPTY + slot), ((pos / C::NSLOT) & 1) ^ 1, abort_flag, status);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(C::B_SLOT_FULL + slot), C::SLOT_BYTES);
-                    __syncwarp();
-                    if (lane < boxes) {
-                        const uint32_t dst = sbase + C::SMEM_SLOTS + slot * C::SLOT_BYTES + box * p.box_rows * 128;
-#pragma unroll
-                        for (int c = 0; c < C::CH; ++c)
-                            tma_load_4d(dst + c * C::BOX_BYTES, map, bar(C::B_SLOT_FULL + slot),
-                                        s * C::SC + c * 64, h, row, id);
-                    }
-                    issued = ++pos;
-                }
+                return id >= 0 && id < p.num_blocks ? id * p.place_block + h * p.place_head : p.places;
             };
             while (ok && walk.next(p, pc)) {
                 if (pc.n == 0) continue;
-                // Consumption order: K(0) .. K(NSB - 1), then V(j), K(j + NSB).
-                int next_id = page_of(pc.kt);
-                int ids[C::NSB];
-                for (int jj = 0; jj < C::NSB && jj < pc.n && ok; ++jj) {
-                    const int id = next_id;
-                    if (jj + 1 < pc.n) next_id = page_of(pc.kt + jj + 1);
-                    load_tile(&tmap_k, pc.kt + jj, id, pc.h);
-                    if constexpr (C::NSB == 2) ids[jj] = id; else ids[0] = id;
-                }
-                for (int j = 0; j < pc.n && ok; ++j) {
-                    load_tile(&tmap_v, pc.kt + j, ids[0], pc.h);
-                    const int jn = j + C::NSB;
-                    int id = 0;
-                    if (jn < pc.n && ok) {
-                        id = next_id;
-                        if (jn + 1 < pc.n) next_id = page_of(pc.kt + jn + 1);
-                        load_tile(&tmap_k, pc.kt + jn, id, pc.h);
+                int next = place_of(pc.kt, pc.h);
+                int j = 0;  // this warp's next tile
+                // The slots of one tile of K or V, in order of consumption.  Both warps
+                // wait for every slot, so that neither can be a phase ahead.
+                auto tile = [&](bool v) {
+                    const bool load = v == is_v;
+                    const int place = next;
+                    if (load && j + 1 < pc.n) next = place_of(pc.kt + j + 1, pc.h);
+                    const int eight = (((pc.kt + j) * C::BN + box * p.box_rows) & (p.block - 1)) >> 3;
+                    for (int s = 0; s < C::SUB && ok; ++s) {
+                        const int slot = pos % C::NSLOT;
+                        ok = warp_wait(bar(C::B_SLOT_EMPTY + slot), ((pos / C::NSLOT) & 1) ^ 1, abort_flag, status);
+                        if (!ok) return;
+                        if (load) {
+                            if (lane == 0) mbar_arrive_expect_tx(bar(C::B_SLOT_FULL + slot), C::SLOT_BYTES);
+                            __syncwarp();
+                            if (lane < boxes)
+                                tma_load_5d(sbase + C::SMEM_SLOTS + slot * C::SLOT_BYTES + box * (p.box_rows / 8) * C::GROUP_BYTES,
+                                            map, bar(C::B_SLOT_FULL + slot), 0, 0, s * C::CH, eight, place);
+                        }
+                        mine = mine << 1 | (load ? 1u : 0u);
+                        ++pos;
                     }
-                    if constexpr (C::NSB == 2) {
-                        ids[0] = ids[1];
-                        ids[1] = id;
-                    } else {
-                        ids[0] = id;
-                    }
+                    if (load) ++j;
+                };
+                for (int i = 0; i < C::NSB && i < pc.n; ++i) tile(false);
+                for (int i = 0; i < pc.n && ok; ++i) {
+                    tile(true);
+                    if (i + C::NSB < pc.n && ok) tile(false);
                 }
             }
             if (!ok && lane == 0)  // let the loads in flight land before the CTA ends
-                for (int q = issued > C::NSLOT ? issued - C::NSLOT : 0; q < issued; ++q)
-                    drain_wait(bar(C::B_SLOT_FULL + q % C::NSLOT), (q / C::NSLOT) & 1);
+                for (int i = 0; i < C::NSLOT && i < pos; ++i)
+                    if (mine >> i & 1)
+                        drain_wait(bar(C::B_SLOT_FULL + (pos - 1 - i) % C::NSLOT), ((pos - 1 - i) / C::NSLOT) & 1);
         }
         __syncwarp();
     } else if (warp == C::MMA_WARP) {
@@ -275,17 +269,18 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, C::BN, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, C::SC, true);
             const uint64_t dq0 = smem_desc_sw128(sbase, 16, 1024);
-            const uint64_t dk0 = smem_desc_sw128(sbase + C::SMEM_SLOTS, 16, 1024);
-            const uint64_t dv0 = smem_desc_sw128(sbase + C::SMEM_SLOTS, C::BOX_BYTES, 1024);
+            const uint64_t dk0 = smem_desc_sw128(sbase + C::SMEM_SLOTS, 16, C::GROUP_BYTES);
+            const uint64_t dv0 = smem_desc_sw128(sbase + C::SMEM_SLOTS, 1024, C::GROUP_BYTES);
             // Part s of S = Q K^T: head-dim columns [s SC, (s + 1) SC).
             auto issue_qk = [&](int q, int b, int s, int slot) {
                 const uint32_t d_tmem = tmem_base + (q * C::NSB + b) * C::BN;
-                const uint64_t dq = dq0 + ((q * C::Q_TILE_BYTES + s * C::CH * C::BOX_BYTES) >> 4);
+                const uint64_t dq = dq0 + ((q * C::Q_TILE_BYTES + s * C::CH * C::Q_CHUNK_BYTES) >> 4);
                 const uint64_t dk = dk0 + ((slot * C::SLOT_BYTES) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < C::SC / 16; ++kk) {
-                    const uint32_t o = ((kk >> 2) * C::BOX_BYTES + (kk & 3) * 32) >> 4;
-                    mma_bf16_ss(d_tmem, dq + o, dk + o, idesc_qk, s > 0 || kk > 0 ? 1u : 0u);
+                    const uint32_t qo = ((kk >> 2) * C::Q_CHUNK_BYTES + (kk & 3) * 32) >> 4;
+                    const uint32_t ko = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+                    mma_bf16_ss(d_tmem, dq + qo, dk + ko, idesc_qk, s > 0 || kk > 0 ? 1u : 0u);
                 }
             };
             // Part s of O += P V (columns [s SC, ..)) over keys [64 half, 64 half + 64),
@@ -293,10 +288,10 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             auto issue_pv = [&](int q, int b, int s, int slot, int half, bool acc) {
                 const uint32_t d_tmem = tmem_base + C::TMEM_O + q * C::D + s * C::SC;
                 const uint32_t p_tmem = tmem_base + (q * C::NSB + b) * C::BN + half * 64;
-                const uint64_t dv = dv0 + ((slot * C::SLOT_BYTES + half * 64 * 128) >> 4);
+                const uint64_t dv = dv0 + ((slot * C::SLOT_BYTES + half * 8 * C::GROUP_BYTES) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ts(d_tmem, p_tmem + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_pv,
+                    mma_bf16_ts(d_tmem, p_tmem + kk * 8, dv + ((kk * 2 * C::GROUP_BYTES) >> 4), idesc_pv,
                                 acc || kk > 0 ? 1u : 0u);
             };
             int pos = 0, pieces[2] = {0, 0}, done[2] = {0, 0};  // per row tile
@@ -435,7 +430,7 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                 {
                     constexpr int PER = C::D / 8;  // 16-byte pieces of a row
                     const int r_first = pc.row0 + q * 128 + (warp & 3) * 32;
-#pragma unroll 4
+#pragma unroll 8
                     for (int i = lane; i < 32 * PER; i += 32) {
                         const int rr = i / PER, c = i % PER;
                         const int g_row = r_first + rr;
@@ -446,7 +441,7 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                                 p.q + (static_cast<int64_t>(t) * p.Hq + pc.h * p.G + (g_row - t * p.G)) * C::D + c * 8);
                         }
                         const int lr = (warp & 3) * 32 + rr;
-                        st_shared_v4(sbase + q * C::Q_TILE_BYTES + (c >> 3) * C::BOX_BYTES + lr * 128 +
+                        st_shared_v4(sbase + q * C::Q_TILE_BYTES + (c >> 3) * C::Q_CHUNK_BYTES + lr * 128 +
                                          (((c & 7) ^ (lr & 7)) << 4),
                                      x.x, x.y, x.z, x.w);
                     }
@@ -532,11 +527,11 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                             ok = warp_wait(bar(C::B_SLOT_FULL + at % C::NSLOT), (at / C::NSLOT) & 1, abort_flag, status);
                             if (!ok) break;
                             if (key0 + row < pc.lo || key0 + row >= P) {
-                                const uint32_t dst = sbase + C::SMEM_SLOTS + (at % C::NSLOT) * C::SLOT_BYTES + row * 128;
+                                const uint32_t dst = sbase + C::SMEM_SLOTS + (at % C::NSLOT) * C::SLOT_BYTES + (row >> 3) * C::GROUP_BYTES + (row & 7) * 128;
                                 for (int c = 0; c < C::CH; ++c)
 #pragma unroll
                                     for (int u = 0; u < 8; ++u)
-                                        st_shared_v4(dst + c * C::BOX_BYTES + u * 16, 0, 0, 0, 0);
+                                        st_shared_v4(dst + c * 1024 + u * 16, 0, 0, 0, 0);
                             }
                         }
                         if (!ok) break;

@@ -41,20 +41,22 @@ inline bool make_map(CUtensorMap* map, const void* base, int64_t T, int H, int D
     return r == CUDA_SUCCESS;
 }
 
-// 4-D map over a paged bf16 cache [blocks, block, H, D] with D dense and the
-// given element strides: dims (D, H, block, blocks), box (64, 1, rows, 1),
-// 128-byte swizzle; a block outside the cache reads as zero.
-inline bool make_paged_map(CUtensorMap* map, const void* base, int64_t blocks, int block, int H, int D,
-                           int64_t block_stride, int64_t token_stride, int64_t head_stride, int box_rows) {
+// 5-D map over a paged bf16 cache [blocks, block, H, D] with D dense and the
+// given token stride: dims (64 columns, 8 tokens, D / 64 column chunks, block / 8,
+// places), where place n begins n * place_stride elements into the cache (its
+// blocks and heads; a place outside reads as zero).  Box (64, 8, box_chunks,
+// box_rows / 8, 1), 128-byte swizzle.
+inline bool make_paged_map(CUtensorMap* map, const void* base, int block, int D, int64_t token_stride,
+                           int64_t place_stride, int64_t places, int box_rows, int box_chunks) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
-                          static_cast<cuuint64_t>(block), static_cast<cuuint64_t>(blocks)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(token_stride) * 2,
-                             static_cast<cuuint64_t>(block_stride) * 2};
-    cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_rows), 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+    cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(D) / 64, static_cast<cuuint64_t>(block) / 8,
+                          static_cast<cuuint64_t>(places)};
+    cuuint64_t strides[4] = {static_cast<cuuint64_t>(token_stride) * 2, 128, static_cast<cuuint64_t>(token_stride) * 16,
+                             static_cast<cuuint64_t>(place_stride) * 2};
+    cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(box_chunks), static_cast<cuuint32_t>(box_rows / 8), 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims,
                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
