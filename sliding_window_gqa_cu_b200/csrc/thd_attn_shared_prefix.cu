@@ -35,146 +35,175 @@ using thd::SpParams;
 // and can be captured); one per device.
 __device__ int g_sp_status;
 
-// Adds up the parts of every row in a fixed order.  A warp takes 8 consecutive
-// rows of a kv head x 16 columns, a thread four columns of a row, eight parts at
-// a time: the parts are a few MB in L2 and the kernel is bound by the latency of
-// its loads (plan, then places, then parts), so all that can be are issued
-// together.
+// Adds up the parts of every row in a fixed order.  A CTA takes 8 consecutive rows
+// of a kv head, a warp 16 columns of their parts of the prefix or of their own
+// pages, a thread four columns of a row.  The parts are a few MB in L2 and the
+// kernel is bound by the latency of its loads (plan, then places, then parts): 16
+// threads find the rows' places for all, and four parts are loaded at a time.
+// (Nothing branches on a part's maximum: the compiler would move the loads behind
+// the branch, one latency after the other.)
 template <int D>
-__global__ void __launch_bounds__(256) thd_sp_merge_kernel(const SpParams p) {
+__global__ void __launch_bounds__(512) thd_sp_merge_kernel(const SpParams p) {
     constexpr int NT = thd::PrefixConfig<D>::NT;
-    constexpr int BATCH = 8;
-    const int lane = threadIdx.x & 31;
-    const int groups = (p.rows + 7) / 8;
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int h = static_cast<int>(w / groups);
-    const int r = static_cast<int>(w - static_cast<int64_t>(h) * groups) * 8 + (lane & 7);
-    const int c4 = blockIdx.y * 4 + (lane >> 3);
-    const bool here = h < p.Hkv && r < p.rows;
-    const int b = here ? r / p.RB : 0, rr = r - b * p.RB;
-    const int g = r % p.G, head = h * p.G + g;
-    const int64_t t = r / p.G;
-    const int64_t bh = static_cast<int64_t>(b) * p.Hkv + h;
-    const bool quads = p.pre_lanes > 0;  // the prefix's parts are the prefix kernel's
-    const int pre_item = r / p.pg_rows * p.Hkv + h;
-    const int64_t own_item = bh * p.pg_units + rr / p.pg_rows;
-    thd::wait_for_previous_grid();
-    if (!here) return;
-    const int n = thd::sp_own_len(p, b);
-    const float sink = p.sinks != nullptr ? p.sinks[head] * 1.4426950408889634f : -INFINITY;
-    thd::SpPlan plan{0, 0, 0};
-    long long own_begin = 0, pre_begin = 0;
-    if (p.any_keys) {
-        plan = *p.plan;
-        own_begin = p.own_desc[own_item];  // (means nothing for an item without keys)
-        if (p.pg_prefix > 0) pre_begin = p.pgp_desc[pre_item];
-        if (!quads && p.pg_prefix == 0) plan.pre_tiles = 0;
-    }
-    if (n < 0) return;
-
-    // Runs of parts, of the prefix and of the request's pages: the home place,
+    constexpr int BATCH = 4;
+    constexpr int WARPS = D < 128 ? D / 16 : 8;  // of a run
+    // A run of parts, of the prefix or of the request's pages: the home place,
     // then the own places of the following workers.
     struct Run {
-        const float* home;   // of this thread's row and columns
+        const float* home;  // of the row, column 0
         const float2* home_ml;
         const float* cont;
         const float2* cont_ml;
         int64_t part_step, ml_step;
-        int n, home_rows, cont_rows;
-    } run[2];
-    run[0].n = run[1].n = 0;
-    // The item whose `count` units of keys begin at unit x of `units`, which are
-    // cut over `lanes` workers of `step` CTAs each.
-    auto workers = [&](Run& u, long long units, int lanes, long long x, int count, int step, int member, int tile_rows) {
-        const int first = thd::lane_of(units, lanes, x), last = thd::lane_of(units, lanes, x + count - 1);
-        u.n = last - first + 1;
-        u.part_step = static_cast<int64_t>(step) * tile_rows * D;
-        u.ml_step = static_cast<int64_t>(step) * tile_rows;
-        // (places of workers first + 1, .. follow: part 0 is the home place)
-        const int64_t at = (static_cast<int64_t>(first) * step + member) * tile_rows;
-        u.cont += at * D;
-        u.cont_ml += at;
+        int n, home_rows, cont_rows, vacant;
     };
-    if (plan.pre_tiles > 0 && quads) {
-        const int tile = r >> 7, group = tile / NT, q = tile - group * NT, row = r & 127;
-        const long long units = static_cast<long long>((p.pre_groups + p.pre_width - 1) / p.pre_width) * p.Hkv * plan.pre_tiles;
-        const int lanes = static_cast<int>(min(units, static_cast<long long>(p.pre_lanes)));
-        const int64_t at = (static_cast<int64_t>(h) * p.pre_groups + group) * NT + q;
-        run[0].home = p.pre_home + at * (128 * D) + (c4 * 128 + row) * 4;
-        run[0].home_ml = p.pre_home_ml + at * 128 + row;
-        run[0].cont = p.pre_cont + static_cast<int64_t>(q) * (128 * D) + (c4 * 128 + row) * 4;
-        run[0].cont_ml = p.pre_cont_ml + q * 128 + row;
-        workers(run[0], units, lanes, (static_cast<long long>(group / p.pre_width) * p.Hkv + h) * plan.pre_tiles,
-                plan.pre_tiles, p.pre_width, group % p.pre_width, NT * 128);
-    } else if (plan.pre_tiles > 0) {
-        const int row = r % p.pg_rows;
-        run[0].home_rows = run[0].cont_rows = p.pg_rows;
-        run[0].home = p.pgp_home + static_cast<int64_t>(pre_item) * p.pg_rows * D + c4 * 4 * p.pg_rows + row;
-        run[0].home_ml = p.pgp_home_ml + static_cast<int64_t>(pre_item) * p.pg_rows + row;
-        run[0].cont = p.pg_cont + c4 * 4 * p.pg_rows + row;
-        run[0].cont_ml = p.pg_cont_ml + row;
-        workers(run[0], plan.pg_units, plan.pg_lanes, pre_begin + thd::kItemUnits, plan.pre_tiles, 1, 0, p.pg_rows);
+    __shared__ Run runs[2][8];
+    __shared__ float own_part[WARPS][6][32];
+    const int groups = (p.rows + 7) / 8;
+    const int h = blockIdx.x / groups, row0 = (blockIdx.x - h * groups) * 8;
+    const bool quads = p.pre_lanes > 0;  // the prefix's parts are the prefix kernel's
+    thd::wait_for_previous_grid();
+    if (threadIdx.x < 16) {
+        const int which = threadIdx.x >> 3, r = min(row0 + static_cast<int>(threadIdx.x & 7), p.rows - 1);
+        const int b = r / p.RB, rr = r - b * p.RB;
+        const int64_t bh = static_cast<int64_t>(b) * p.Hkv + h;
+        const int pre_item = r / p.pg_rows * p.Hkv + h;
+        const int n = thd::sp_own_len(p, b);
+        thd::SpPlan plan{0, 0, 0};
+        long long begin = 0;  // (means nothing for an item without keys)
+        if (p.any_keys) {
+            plan = *p.plan;
+            if (which == 1) begin = p.own_desc[bh * p.pg_units + rr / p.pg_rows];
+            else if (p.pg_prefix > 0) begin = p.pgp_desc[pre_item];
+            if (!quads && p.pg_prefix == 0) plan.pre_tiles = 0;
+        }
+        Run u;
+        u.n = 0;
+        u.home = u.cont = nullptr;
+        u.home_ml = u.cont_ml = nullptr;
+        u.part_step = u.ml_step = 0;
+        u.home_rows = u.cont_rows = 0;
+        u.vacant = n < 0 ? 1 : 0;
+        long long units = plan.pg_units, x = begin + thd::kItemUnits;
+        int lanes = plan.pg_lanes, count = plan.pre_tiles, step = 1, member = 0, tile_rows = p.pg_rows;
+        if (which == 0 && quads) {
+            const int tile = r >> 7, group = tile / NT, q = tile - group * NT, row = r & 127;
+            const int len = plan.pre_tiles + thd::kItemTiles;
+            units = static_cast<long long>((p.pre_groups + p.pre_width - 1) / p.pre_width) * p.Hkv * len;
+            lanes = thd::sp_prefix_lanes(p, units);
+            x = (static_cast<long long>(group / p.pre_width) * p.Hkv + h) * len + thd::kItemTiles;
+            step = p.pre_width;
+            member = group % p.pre_width;
+            tile_rows = NT * 128;
+            const int64_t at = (static_cast<int64_t>(h) * p.pre_groups + group) * NT + q;
+            u.home = p.pre_home + at * (128 * D) + row * 4;
+            u.home_ml = p.pre_home_ml + at * 128 + row;
+            u.cont = p.pre_cont + static_cast<int64_t>(q) * (128 * D) + row * 4;
+            u.cont_ml = p.pre_cont_ml + q * 128 + row;
+            u.home_rows = u.cont_rows = 128;
+        } else if (which == 0) {
+            const int row = r % p.pg_rows;
+            u.home_rows = u.cont_rows = p.pg_rows;
+            u.home = p.pgp_home + static_cast<int64_t>(pre_item) * p.pg_rows * D + row * 4;
+            u.home_ml = p.pgp_home_ml + static_cast<int64_t>(pre_item) * p.pg_rows + row;
+            u.cont = p.pg_cont + row * 4;
+            u.cont_ml = p.pg_cont_ml + row;
+        } else {
+            const int row = rr % p.pg_rows;
+            count = p.pg_slice == 32 ? thd::sp_own_slices<32>(p, n) : thd::sp_own_slices<16>(p, n);
+            u.home_rows = p.RB;
+            u.cont_rows = p.pg_rows;
+            u.home = p.own_home + bh * p.RB * D + rr * 4;
+            u.home_ml = p.own_home_ml + bh * p.RB + rr;
+            u.cont = p.pg_cont + row * 4;
+            u.cont_ml = p.pg_cont_ml + row;
+        }
+        if (count > 0) {
+            const int first = thd::lane_of(units, lanes, x), last = thd::lane_of(units, lanes, x + count - 1);
+            u.n = last - first + 1;
+            u.part_step = static_cast<int64_t>(step) * tile_rows * D;
+            u.ml_step = static_cast<int64_t>(step) * tile_rows;
+            // (places of workers first + 1, .. follow: part 0 is the home place)
+            const int64_t at = (static_cast<int64_t>(first) * step + member) * tile_rows;
+            u.cont += at * D;
+            u.cont_ml += at;
+        }
+        runs[which][threadIdx.x & 7] = u;
     }
-    const int own = p.pg_slice == 32 ? thd::sp_own_slices<32>(p, n) : thd::sp_own_slices<16>(p, n);
-    if (own > 0) {
-        const int row = rr % p.pg_rows;
-        run[1].home_rows = p.RB;
-        run[1].cont_rows = p.pg_rows;
-        run[1].home = p.own_home + bh * p.RB * D + static_cast<int64_t>(c4) * 4 * p.RB + rr;
-        run[1].home_ml = p.own_home_ml + bh * p.RB + rr;
-        run[1].cont = p.pg_cont + c4 * 4 * p.pg_rows + row;
-        run[1].cont_ml = p.pg_cont_ml + row;
-        workers(run[1], plan.pg_units, plan.pg_lanes, own_begin + thd::kItemUnits, own, 1, 0, p.pg_rows);
-    }
-    float m = sink, l = sink == -INFINITY ? 0.0f : 1.0f;
+    __syncthreads();
+    const int lane = threadIdx.x & 31, r = row0 + (lane & 7), warp = threadIdx.x >> 5;
+    const int which = warp / WARPS;
+    const int c4 = (blockIdx.y * WARPS + warp % WARPS) * 4 + (lane >> 3);
+    float m = -INFINITY, l = 0.0f;
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const Run& u = run[i];
+    {
+        const Run u = runs[which][lane & 7];
+        const float* part = u.home + c4 * 4 * u.home_rows;
+        const float2* ml_at = u.home_ml;
+        const float* cont = u.cont + c4 * 4 * u.cont_rows + u.part_step;
+        const float2* cont_ml = u.cont_ml + u.ml_step;
+        const int n = u.n;
 #pragma unroll 1
-        for (int c0 = 0; c0 < u.n; c0 += BATCH) {
+        for (int c0 = 0; c0 < n; c0 += BATCH) {
             float2 ml[BATCH];
             float4 o[BATCH];
 #pragma unroll
             for (int c = 0; c < BATCH; ++c) {
-                const int k = min(c0 + c, u.n - 1);
-                const float* at = k == 0 ? u.home : u.cont + k * u.part_step;
-                ml[c] = k == 0 ? *u.home_ml : u.cont_ml[k * u.ml_step];
-                if (i == 0 && quads) {
-                    o[c] = *reinterpret_cast<const float4*>(at);
-                } else {
-                    const int rows = k == 0 ? u.home_rows : u.cont_rows;
-                    o[c] = make_float4(at[0], at[rows], at[2 * static_cast<int64_t>(rows)], at[3 * static_cast<int64_t>(rows)]);
+                ml[c] = __ldcg(ml_at);
+                o[c] = __ldcg(reinterpret_cast<const float4*>(part));
+                if (c0 + c >= n) ml[c].x = -INFINITY;  // (the last part again)
+                if (c0 + c + 1 < n) {
+                    part = cont;
+                    ml_at = cont_ml;
+                    cont += u.part_step;
+                    cont_ml += u.ml_step;
                 }
             }
             float top = m;
 #pragma unroll
-            for (int c = 0; c < BATCH; ++c) {
-                if (c0 + c >= u.n) ml[c].x = -INFINITY;
-                top = fmaxf(top, ml[c].x);
-            }
-            const float a = m == -INFINITY ? 0.0f : exp2f(m - top);
+            for (int c = 0; c < BATCH; ++c) top = fmaxf(top, ml[c].x);
+            const float base = top == -INFINITY ? 0.0f : top;
+            const float a = exp2f(m - base);
             m = top;
             l *= a;
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[k] *= a;
 #pragma unroll
             for (int c = 0; c < BATCH; ++c) {
-                if (ml[c].x == -INFINITY) continue;  // (its part may never have been written)
-                const float x = exp2f(ml[c].x - top);
-                l = fmaf(ml[c].y, x, l);
-                acc[0] = fmaf(o[c].x, x, acc[0]);
-                acc[1] = fmaf(o[c].y, x, acc[1]);
-                acc[2] = fmaf(o[c].z, x, acc[2]);
-                acc[3] = fmaf(o[c].w, x, acc[3]);
+                const float x = exp2f(ml[c].x - base);
+                const bool there = x > 0.0f;  // (a part with nothing in it may never have been written)
+                l = fmaf(there ? ml[c].y : 0.0f, x, l);
+                acc[0] = fmaf(there ? o[c].x : 0.0f, x, acc[0]);
+                acc[1] = fmaf(there ? o[c].y : 0.0f, x, acc[1]);
+                acc[2] = fmaf(there ? o[c].z : 0.0f, x, acc[2]);
+                acc[3] = fmaf(there ? o[c].w : 0.0f, x, acc[3]);
             }
         }
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    *reinterpret_cast<uint2*>(p.out + (t * p.Hq + head) * D + c4 * 4) =
-        make_uint2(thd::pack_bf16x2(acc[0] * inv, acc[1] * inv), thd::pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    if (p.lse != nullptr && blockIdx.y == 0 && lane < 8)
-        p.lse[t * p.Hq + head] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (which == 1) {
+        float(&at)[6][32] = own_part[warp - WARPS];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) at[k][lane] = acc[k];
+        at[4][lane] = m;
+        at[5][lane] = l;
+    }
+    __syncthreads();
+    if (which == 1 || r >= p.rows || runs[0][lane & 7].vacant) return;
+    const int t = r / p.G, head = h * p.G + (r - t * p.G);
+    const float sink = p.sinks != nullptr ? p.sinks[head] * 1.4426950408889634f : -INFINITY;
+    const float(&own)[6][32] = own_part[warp];
+    const float top = fmaxf(fmaxf(m, own[4][lane]), sink);
+    const float base = top == -INFINITY ? 0.0f : top;
+    const float x = exp2f(m - base), y = exp2f(own[4][lane] - base);
+    const float sum = l * x + own[5][lane] * y + exp2f(sink - base);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = (acc[k] * x + own[k][lane] * y) * inv;
+    const int64_t orow = static_cast<int64_t>(t) * p.Hq + head;
+    *reinterpret_cast<uint2*>(p.out + orow * D + c4 * 4) =
+        make_uint2(thd::pack_bf16x2(acc[0], acc[1]), thd::pack_bf16x2(acc[2], acc[3]));
+    if (p.lse != nullptr && c4 == 0)
+        p.lse[orow] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 constexpr int kMaxUnits = 4096;
@@ -292,11 +321,13 @@ bool launch_prefix(const SpParams& p, const CUtensorMap& mk, const CUtensorMap& 
 }
 
 template <int D, int NR, int WR>
-bool launch_paged(const SpParams& p, int* status, bool early, cudaStream_t stream) {
+bool launch_paged(SpParams& p, int* status, bool early, cudaStream_t stream) {
     using C = thd::PagedConfig<D, NR, WR>;
+    p.pg_slice = C::KS;
     static std::atomic<uint64_t> done{0};
     return allow_smem(thd::thd_sp_paged_kernel<C>, C::SMEM_BYTES, done) &&
-           launch_early(thd::thd_sp_paged_kernel<C>, dim3(p.pg_ctas), C::THREADS, C::SMEM_BYTES, stream, early, p, status);
+           launch_early(thd::thd_sp_paged_kernel<C>, dim3(p.pg_ctas), C::THREADS, C::SMEM_BYTES, stream, early,
+                        static_cast<const SpParams&>(p), status);
 }
 
 struct Maps {
@@ -330,8 +361,9 @@ int launch_all(SpParams p, const Maps& maps, cudaStream_t stream) {
         if (!ok) return THD_ERR_CUDA;
         early = true;
     }
-    const int64_t warps = static_cast<int64_t>(p.Hkv) * ((p.rows + 7) / 8);
-    if (!launch_early(thd_sp_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8), D / 16), 256, 0, stream, early, p))
+    const int64_t ctas = static_cast<int64_t>(p.Hkv) * ((p.rows + 7) / 8);
+    if (!launch_early(thd_sp_merge_kernel<D>, dim3(static_cast<unsigned>(ctas), D > 128 ? D / 128 : 1),
+                      D < 128 ? 4 * D : 512, 0, stream, early, p))
         return THD_ERR_CUDA;
     return THD_OK;
 }
@@ -442,7 +474,6 @@ extern "C" int thd_attn_shared_prefix(const void* q, const void* k_cache, const 
     p.pgp_desc = i8(y.pgp_desc);
     p.pg_cont = f(y.pg_cont);
     p.pg_cont_ml = f2(y.pg_cont_ml);
-    p.pg_slice = D * (y.pg_rows == 8 || D == 256 ? 1 : 2) <= 128 ? 32 : 16;
     Maps maps{};
     if (any_keys && p.pre_lanes > 0) {
         const int64_t bs = num_blocks > 1 ? block_stride : 0, hs = Hkv > 1 ? head_stride : 0;

@@ -8,17 +8,16 @@
 // Work.  A unit is one tile of keys of one item (a row tile of one kv head).
 // A kernel's units are numbered item by item and cut into as many equal
 // consecutive ranges as it has lanes (a CTA, or a group of CTAs in step), so
-// every lane gets the same number whatever the lengths.  What a lane does of
+// every lane gets the same number whatever the lengths.  An item counts a few
+// units more, before its keys, for what it costs to start and end it.  What a lane does of
 // one item is a piece.  Its unnormalised output, running maximum (in units of
 // log2) and sum go to the item's home place if the piece holds the item's first
 // tile, else to the CTA's own place (only a lane's first piece can begin inside
 // an item); the merge kernel adds them up in a fixed order.
 //
-// A partial tile is stored with the rows side by side, [D / 4][rows][4] fp32 by
-// the prefix kernel (a thread holds a row) and [D][rows] by the paged kernel (a
-// quad of threads holds 8 rows of a column), with (maximum, sum) per row beside
-// it, so that threads with neighbouring rows write whole sectors and the merge
-// kernel reads them.
+// A partial tile is stored as [D / 4][rows][4] fp32 with (maximum, sum) per row
+// beside it: threads that hold neighbouring rows then write, and the merge kernel
+// reads, whole lines.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -29,6 +28,10 @@
 namespace thd {
 
 constexpr int kSpLanes = 148;  // CTAs of the prefix kernel (one per SM)
+// What starting and ending an item costs, in units: key tiles of the prefix
+// kernel, slices of the paged kernel.
+constexpr int kItemTiles = 4;
+constexpr int kItemUnits = 1;
 
 // What the kernels derived from the lengths, for the merge kernel.
 struct SpPlan {
@@ -82,6 +85,11 @@ struct SpParams {
     SpPlan* plan;
 };
 
+// 16 bytes into shared memory, zeros if !there.
+__device__ __forceinline__ void load16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
 // (32-bit division where it is enough: the 64-bit one takes some 100 instructions.)
 // First unit of lane l when `units` are cut into `lanes` ranges (lanes <= units,
 // so that none is empty).
@@ -96,6 +104,12 @@ __device__ __forceinline__ int lane_of(long long units, int lanes, long long x) 
     const unsigned long long at = static_cast<unsigned long long>(x + 1) * lanes - 1;
     if (at >> 32 == 0) return static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(units));
     return static_cast<int>(at / static_cast<unsigned long long>(units));
+}
+
+// Lanes that the prefix kernel's units are cut over: some units each (parts of
+// fewer tiles would cost more traffic than they share out).
+__device__ __forceinline__ int sp_prefix_lanes(const SpParams& p, long long units) {
+    return static_cast<int>(min((units + kItemTiles + 1) / (kItemTiles + 2), static_cast<long long>(p.pre_lanes)));
 }
 
 __device__ __forceinline__ int sp_prefix_len(const SpParams& p) {

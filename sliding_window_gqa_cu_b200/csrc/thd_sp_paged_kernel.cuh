@@ -11,8 +11,8 @@
 //
 // A worker is WR warps of 8 NR rows each, which share a ring of slots (a K or V
 // slice of KS keys each) and refill a slot as soon as it has been read.  Workers
-// never wait for each other.  16 KB a warp, 64 KB a CTA are in flight: three
-// CTAs on an SM, or one beside the prefix kernel.  The loads are cp.async: a page
+// never wait for each other.  16 KB a warp, 64 KB a CTA are in flight, three
+// CTAs on an SM.  The loads are cp.async: a page
 // of 16 tokens is too small a box for TMA, which took 75 to 85 ns per box and SM
 // here (24 to 27 GB/s of the SM's share of 44).
 //
@@ -37,11 +37,6 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-// 16 bytes into shared memory, zeros if !there.
-__device__ __forceinline__ void load16(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-
 // Arrives on the barrier when this thread's loads so far have landed.
 __device__ __forceinline__ void loads_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -63,12 +58,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// What starting and ending an item costs, in units.
-constexpr int kItemUnits = 1;
-// Units that a worker gets at least: fewer would make more parts to add up than
-// they save (a part costs the merge kernel about as much as a slice takes here).
-constexpr int kWorkerUnits = 4;
-
 template <int D_, int NR_, int WR_>
 struct PagedConfig {
     static constexpr int D = D_;
@@ -79,13 +68,12 @@ struct PagedConfig {
     static constexpr int KS = D * NR <= 128 ? 32 : 16;  // keys of a slice (what the registers hold)
     static constexpr int ROW_BYTES = D * 2;
     static constexpr int SLOT_BYTES = KS * D * 2;
-    static constexpr int NSLOT = 16384 * WR / SLOT_BYTES;
+    static constexpr int RING_BYTES = 65536;
+    static constexpr int NSLOT = RING_BYTES / 4 * WR / SLOT_BYTES;
     static constexpr int THREADS = 128;
-    // CTAs on an SM: 128 registers a thread, so that one CTA also fits beside
-    // the prefix kernel (12 warp places of 128 registers).
-    static constexpr int RESIDENT = D == 256 ? 3 : 4;
+    static constexpr int RESIDENT = 3;  // CTAs on an SM
 
-    static constexpr int SMEM_BAR = 65536;
+    static constexpr int SMEM_BAR = RING_BYTES;
     static constexpr int B_FULL = 0, B_EMPTY = WORKERS * NSLOT, NUM_BARS = 2 * WORKERS * NSLOT;
     static constexpr int SMEM_START = SMEM_BAR + NUM_BARS * 8;  // int64 [16]
     static constexpr int SMEM_ABORT = SMEM_START + 128;
@@ -101,7 +89,7 @@ struct PagedPiece {
     int first, end;      // keys that some row sees: [first, end)
     int row0, rows;      // rows of the tile
     int h;
-    float* part;         // [D][part_rows]
+    float* part;         // [D / 4][part_rows][4]
     float2* ml;
     int part_rows;
 };
@@ -177,7 +165,7 @@ struct PagedWalk {
                 pc.rows = min(C::ROWS, p.RB - u * C::ROWS);
                 pc.slice = pc.first / C::KS;
                 const int64_t bh = static_cast<int64_t>(b) * p.Hkv + pc.h;
-                pc.part = p.own_home + bh * p.RB * C::D + u * C::ROWS;
+                pc.part = p.own_home + bh * p.RB * C::D + u * C::ROWS * 4;
                 pc.ml = p.own_home_ml + bh * p.RB + u * C::ROWS;
                 pc.part_rows = p.RB;
                 desc = p.own_desc + bh * p.pg_units + u;
@@ -236,12 +224,13 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
         auto units_of = [&](int n) -> long long {
             return n > 0 ? static_cast<long long>(sp_own_slices<C::KS>(p, n) + kItemUnits) * unit : 0;
         };
-        int least = 0x7fffffff;
+        int least = 0x7fffffff, longest = 0;  // own length; slices of an item
         long long mine = 0;
         for (int b = b0; b < b1; ++b) {
             const int n = sp_own_len(p, b);
             mine += units_of(n);
             if (n >= 0) least = min(least, n);
+            if (n > 0) longest = max(longest, sp_own_slices<C::KS>(p, n));
         }
         long long incl = mine;
 #pragma unroll
@@ -250,15 +239,17 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
             if (lane >= o) incl += y;
         }
         least = __reduce_min_sync(0xffffffffu, least);
+        longest = __reduce_max_sync(0xffffffffu, longest);
         if (lane == 31) start[warp] = incl;
-        if (lane == 0) start[4 + warp] = least;
+        if (lane == 0) start[4 + warp] = static_cast<long long>(longest) << 32 | least;
         __syncthreads();
         long long before = incl - mine, total = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             if (w < warp) before += start[w];
             total += start[w];
-            least = min(least, static_cast<int>(start[4 + w]));
+            least = min(least, static_cast<int>(start[4 + w] & 0x7fffffff));
+            longest = max(longest, static_cast<int>(start[4 + w] >> 32));
         }
         const int lo = least == 0x7fffffff ? P : sp_first_key(p, P + least - p.n_q);
         walk.P = P;
@@ -268,7 +259,14 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
         walk.pre_units = walk.pre_slices > 0
                              ? static_cast<long long>(p.pg_prefix) * p.Hkv * (walk.pre_slices + kItemUnits) : 0;
         const long long units = walk.pre_units + total;
-        const int lanes = static_cast<int>(min((units + kWorkerUnits - 1) / kWorkerUnits,
+        // Units that a worker gets at least.  A part more costs its traffic (written
+        // and read, 2 ROWS / KS slices' worth: a quarter of the slices' at most) and,
+        // for the item with most parts, time in the merge kernel: some 0.15 us a part
+        // against 0.7 us a slice here, so the time of u units and longest / u parts is
+        // least near the root of longest / 5.
+        longest = max(longest, walk.pre_slices);
+        const int least_units = max(max(4, 8 * C::ROWS / C::KS), static_cast<int>(sqrtf(0.2f * longest)));
+        const int lanes = static_cast<int>(min((units + least_units - 1) / least_units,
                                                static_cast<long long>(p.pg_ctas) * C::WORKERS));
         // Where each worker's range begins among the own units.
 #pragma unroll
@@ -577,8 +575,9 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
                     if (rr < pc.rows) {
 #pragma unroll
                         for (int i = 0; i < C::D / 16; ++i) {
-                            pc.part[static_cast<int64_t>(i * 16 + r8) * pc.part_rows + rr] = acc[i][t][e];
-                            pc.part[static_cast<int64_t>(i * 16 + 8 + r8) * pc.part_rows + rr] = acc[i][t][e + 2];
+                            const int64_t q4 = i * 4 + (r8 >> 2);
+                            pc.part[(q4 * pc.part_rows + rr) * 4 + (r8 & 3)] = acc[i][t][e];
+                            pc.part[((q4 + 2) * pc.part_rows + rr) * 4 + (r8 & 3)] = acc[i][t][e + 2];
                         }
                         if (r8 == 0) pc.ml[rr] = make_float2(m[t][e], x);
                     }

@@ -8,22 +8,18 @@
 // NT = 2 row tiles per CTA (D <= 128) take turns: while one tile's scores are
 // in the softmax the tensor core works on the other's.  At D = 256 the two
 // accumulators would fill TMEM, so one row tile with two score buffers does
-// the same.
+// the same, and two threads share a row.
 //
 // Work split: groups of NT * 128 rows; `pre_width` groups of a kv head walk the
 // same keys in step (one CTA each, so that K and V come from L2 for all but the
 // first), and the sequence (bundle of groups, kv head, key tile) is cut into
 // equal ranges, one per lane of CTAs.
 //
-// Warps: 4 NT softmax warps (thread = row), a TMA producer for K and one for V, an
-// MMA issuer.  A TMA instruction takes about 50 ns whatever its size, so one box
-// holds a page's tokens (128 at most) x all columns of a slot: [tokens / 8]
-// [column chunk][8 tokens][64 columns], whose groups of 8 tokens have one stride
-// over the pages of a tile, as the matrix descriptors need it.
-// The kernel leaves registers and, at D <= 128, shared memory for a CTA of the
-// paged kernel on the same SM: that one is bound by memory.  For that a
-// thread holds half a row of scores at a time; the first half is read from TMEM
-// twice (once for the maximum).
+// Warps: 8 softmax warps (a thread a row; D = 256: two), a TMA producer for K and
+// one for V, an MMA issuer.  A TMA box holds a page's tokens (128 at most) x all
+// columns of a slot: [tokens / 8][column chunk][8 tokens][64 columns], whose
+// groups of 8 tokens have one stride over the pages of a tile, as the matrix
+// descriptors need it.
 #pragma once
 
 #include "thd_attn_kernel.cuh"
@@ -40,20 +36,19 @@ struct PrefixConfig {
     static constexpr int SC = D < 128 ? D : 128;  // columns of a ring slot
     static constexpr int SUB = D / SC;            // slots of a K or V tile
     static constexpr int CH = SC / 64;            // 128-byte chunks of a slot row
-    static constexpr int NSLOT = D == 64 ? 6 : D == 128 ? 3 : 4;
+    static constexpr int NSLOT = D == 64 ? 10 : 5;
+    static constexpr int HALVES = D == 256 ? 2 : 1;  // threads that share a row's softmax
+    static constexpr int COLS = BN / HALVES;         // keys of a tile that a thread takes,
+    static constexpr int CK = COLS / 2;              // in two chunks of this many
     static constexpr int Q_CHUNK_BYTES = 128 * 128;    // one chunk of a Q tile
     static constexpr int GROUP_BYTES = CH * 1024;      // 8 keys of a slot, chunk by chunk
     static constexpr int SLOT_BYTES = BN * SC * 2;
     static constexpr int Q_TILE_BYTES = 128 * D * 2;
-    static constexpr int SOFTMAX_WARPS = 4 * NT;
+    static constexpr int SOFTMAX_WARPS = 4 * NT * HALVES;
     static constexpr int K_WARP = SOFTMAX_WARPS;
     static constexpr int V_WARP = SOFTMAX_WARPS + 1;
     static constexpr int MMA_WARP = SOFTMAX_WARPS + 2;
     static constexpr int THREADS = (SOFTMAX_WARPS + 3) * 32;
-    // Threads that the register budget is made for: 128 registers a thread leave
-    // a quarter of the registers to a CTA of the paged kernel.
-    static constexpr int BOUND = D == 256 ? 384 : 512;
-
     static constexpr int TMEM_O = NT * NSB * BN;
     static_assert(TMEM_O + NT * D <= 512, "TMEM budget exceeded");
 
@@ -61,7 +56,7 @@ struct PrefixConfig {
     static constexpr int B_SLOT_FULL = B_Q_FULL + NT;
     static constexpr int B_SLOT_EMPTY = B_SLOT_FULL + NSLOT;
     static constexpr int B_S_FULL = B_SLOT_EMPTY + NSLOT;     // [NT][NSB]
-    static constexpr int B_P_FULL = B_S_FULL + NT * NSB;      // [NT][2]: keys 64.. first, then 0..63
+    static constexpr int B_P_FULL = B_S_FULL + NT * NSB;      // [NT][2]: P of 64 keys written, O rescaled
     static constexpr int B_O_FULL = B_P_FULL + 2 * NT;        // [NT]
     static constexpr int B_DRAIN = B_O_FULL + NT;
     static constexpr int NUM_BARS = B_DRAIN + 1;
@@ -69,9 +64,11 @@ struct PrefixConfig {
     static constexpr int SMEM_SLOTS = NT * Q_TILE_BYTES;
     static constexpr int SMEM_BAR = SMEM_SLOTS + NSLOT * SLOT_BYTES;
     static constexpr int SMEM_MIN = SMEM_BAR + NUM_BARS * 8;  // [warp]: least own length
-    static constexpr int SMEM_TMEM_SLOT = SMEM_MIN + 16 * 4;
+    static constexpr int SMEM_XCH = SMEM_MIN + 32 * 4;          // float [NSB][NT][2][128]: maxima (sums) of two threads of a row
+    static constexpr int SMEM_TMEM_SLOT = SMEM_XCH + (HALVES > 1 ? NSB * NT * 2 * 128 * 4 : 0);
     static constexpr int SMEM_ABORT = SMEM_TMEM_SLOT + 4;
     static constexpr int SMEM_BYTES = SMEM_ABORT + 4;
+    static_assert(SMEM_BYTES <= 232448 && NSLOT >= 2 * SUB, "shared memory budget");
 };
 
 // One CTA's share of one item.
@@ -87,21 +84,23 @@ struct PrefixPiece {
 template <class C>
 struct PrefixWalk {
     long long x, x1;
-    int member, first_tile, n_tiles, prefix, n_items;
+    int member, first_tile, n_tiles, prefix;
 
     __device__ __forceinline__ bool next(const SpParams& p, PrefixPiece& pc) {
         while (x < x1) {
-            const int item = static_cast<int>(x / n_tiles);
-            const int at = static_cast<int>(x - static_cast<long long>(item) * n_tiles);
-            const int cnt = static_cast<int>(min(static_cast<long long>(n_tiles - at), x1 - x));
+            const int len = n_tiles + kItemTiles;
+            const int item = x <= 0x7fffffff ? static_cast<int>(x) / len : static_cast<int>(x / len);
+            const int at = static_cast<int>(x - static_cast<long long>(item) * len);
+            const int cnt = static_cast<int>(min(static_cast<long long>(len - at), x1 - x));
+            const int t0 = max(at - kItemTiles, 0), t1 = at + cnt - kItemTiles;
             x += cnt;
             pc.h = item % p.Hkv;
             pc.group = item / p.Hkv * p.pre_width + member;
-            if (pc.group >= p.pre_groups) continue;
+            if (pc.group >= p.pre_groups || t1 <= t0) continue;
             pc.row0 = pc.group * (C::NT * 128);
             const int left = p.rows - pc.row0;
             pc.tiles = C::NT == 2 && left > 128 ? 2 : 1;
-            pc.home = at == 0;
+            pc.home = t0 == 0;
             int lo = 0;
             if (p.window > 0) {
                 // least own length of the group's requests
@@ -116,9 +115,9 @@ struct PrefixWalk {
                 lo = n == 0x7fffffff ? prefix : sp_first_key(p, prefix + n - p.n_q);
             }
             pc.lo = lo;
-            const int k0 = max(first_tile + at, lo / C::BN);
+            const int k0 = max(first_tile + t0, lo / C::BN);
             pc.kt = k0;
-            pc.n = max(0, first_tile + at + cnt - k0);
+            pc.n = max(0, first_tile + t1 - k0);
             if (lo >= prefix) pc.n = 0;
             return true;
         }
@@ -127,7 +126,7 @@ struct PrefixWalk {
 };
 
 template <class C>
-__global__ void __launch_bounds__(C::BOUND, 1)
+__global__ void __launch_bounds__(C::THREADS, 1)
 thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                      const SpParams p, int* status) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -143,7 +142,7 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
 
     if (threadIdx.x == 0) {
         for (int q = 0; q < C::NT; ++q) {
-            mbar_init(bar(C::B_Q_FULL + q), 4);
+            mbar_init(bar(C::B_Q_FULL + q), 4 * C::HALVES);
             mbar_init(bar(C::B_P_FULL + 2 * q), 4);
             mbar_init(bar(C::B_P_FULL + 2 * q + 1), 4);
             mbar_init(bar(C::B_O_FULL + q), 1);
@@ -198,8 +197,8 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         walk.member = blockIdx.x % p.pre_width;
         const int my_lane = blockIdx.x / p.pre_width;
         const long long units = static_cast<long long>((p.pre_groups + p.pre_width - 1) / p.pre_width) * p.Hkv *
-                                walk.n_tiles;
-        const int lanes = static_cast<int>(min(units, static_cast<long long>(p.pre_lanes)));
+                                (walk.n_tiles > 0 ? walk.n_tiles + kItemTiles : 0);
+        const int lanes = sp_prefix_lanes(p, units);
         walk.x = my_lane < lanes ? lane_begin(units, lanes, my_lane) : 0;
         walk.x1 = my_lane < lanes ? lane_begin(units, lanes, my_lane + 1) : 0;
         if (blockIdx.x == 0 && threadIdx.x == 0) p.plan->pre_tiles = walk.n_tiles;
@@ -284,14 +283,14 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                 }
             };
             // Part s of O += P V (columns [s SC, ..)) over keys [64 half, 64 half + 64),
-            // whose P lies in the score columns [64 half, 64 half + 32).
+            // whose P lies in the first half of every CK score columns.
             auto issue_pv = [&](int q, int b, int s, int slot, int half, bool acc) {
                 const uint32_t d_tmem = tmem_base + C::TMEM_O + q * C::D + s * C::SC;
                 const uint32_t p_tmem = tmem_base + (q * C::NSB + b) * C::BN + half * 64;
                 const uint64_t dv = dv0 + ((slot * C::SLOT_BYTES + half * 8 * C::GROUP_BYTES) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ts(d_tmem, p_tmem + kk * 8, dv + ((kk * 2 * C::GROUP_BYTES) >> 4), idesc_pv,
+                    mma_bf16_ts(d_tmem, p_tmem + kk * 16 / C::CK * C::CK + kk * 16 % C::CK / 2, dv + ((kk * 2 * C::GROUP_BYTES) >> 4), idesc_pv,
                                 acc || kk > 0 ? 1u : 0u);
             };
             int pos = 0, pieces[2] = {0, 0}, done[2] = {0, 0};  // per row tile
@@ -333,6 +332,7 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                             // commit: S(j + 1) ready also says that O holds PV(j).
                             ok = wait_slot(vpos);
                             for (int q = 0; q < pc.tiles && ok; ++q) {
+                                // (the second chunk is published first)
                                 for (int half = 1; half >= 0 && ok; --half) {
                                     ok = wait(C::B_P_FULL + 2 * q + half, (done[q] + j) & 1);
                                     if (!ok) break;
@@ -356,14 +356,14 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                             pos += more ? 2 : 1;
                         } else {
                             const int b = (done[0] + j) % C::NSB;
-                            for (int half = 1; half >= 0 && ok; --half)
+                            for (int half = 0; half < 2 && ok; ++half)
                                 ok = wait(C::B_P_FULL + half, (done[0] + j) & 1);
                             for (int s = 0; s < C::SUB && ok; ++s) {
                                 ok = wait_slot(vpos + s);
                                 if (!ok) break;
                                 tc_fence_after();
-                                issue_pv(0, b, s, (vpos + s) % C::NSLOT, 1, j > 0);
-                                issue_pv(0, b, s, (vpos + s) % C::NSLOT, 0, true);
+                                issue_pv(0, b, s, (vpos + s) % C::NSLOT, 0, j > 0);
+                                issue_pv(0, b, s, (vpos + s) % C::NSLOT, 1, true);
                                 if (s == C::SUB - 1) mma_commit(bar(C::B_O_FULL));
                                 mma_commit(bar(C::B_SLOT_EMPTY + (vpos + s) % C::NSLOT));
                             }
@@ -389,19 +389,70 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
-        const int q = warp >> 2;
+        const int q = warp / (4 * C::HALVES), half = (warp >> 2) % C::HALVES;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t o_tmem = lane_base + C::TMEM_O + q * C::D;
+        // This warp's share of O and, in a score buffer, of S and P.
+        constexpr int O_COLS = C::D / C::HALVES;
+        const uint32_t o_tmem = lane_base + C::TMEM_O + q * C::D + half * O_COLS;
+        const uint32_t s_tmem0 = lane_base + q * C::NSB * C::BN + half * C::COLS;
+        float* xch = reinterpret_cast<float*>(smem + C::SMEM_XCH) + q * 256 + row;
+        const uint32_t pair_bar = 1 + q * 4 + (warp & 3);  // of the two warps that share rows
         const float sl2 = p.scale_log2;
-        const int valid_pages_lane = (lane * 16) >> p.block_shift;  // page of 16-key group `lane` of a tile
         constexpr float kTau = 8.0f;  // rescale O only when the maximum grows by more than 2^8
-        int pos = 0, pieces = 0, done = 0;
+        int pos = 0, pieces = 0, done = 0, turn = 0;
         bool ok = !skip;
-        while (ok && walk.next(p, pc)) {
+        // The two threads of a row swap a value.  (With one score buffer S(j + 1) is only
+        // ready when both have published P(j), so the place is free again; with two
+        // they take turns.)  A warp that gives up still arrives (below), and its
+        // partner sees the flag before it could wait again.
+        auto swap = [&](float v) -> float {
+            float* at = xch + turn % C::NSB * (C::NT * 256);
+            ++turn;
+            at[half * 128] = v;
+            if (*abort_flag != 0) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return v;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+            return at[(1 - half) * 128];
+        };
+        // Q rows of a piece into shared memory, 128-byte swizzled: every warp of a row
+        // tile its share.
+        auto load_q = [&](const PrefixPiece& c) {
+            constexpr int PER = C::D / 8;  // 16-byte pieces of a row
+            constexpr int SHARE = 32 / C::HALVES;
+            const int l_first = warp % (4 * C::HALVES) * SHARE, r_first = c.row0 + q * 128 + l_first;
+            int64_t off = 0;  // thread t: row r_first + t
+            const int mine = min(r_first + lane % SHARE, p.rows - 1), t = mine / p.G;
+            off = (static_cast<int64_t>(t) * p.Hq + c.h * p.G + (mine - t * p.G)) * C::D;
+#pragma unroll
+            for (int i = 0; i < SHARE * PER / 32; ++i) {
+                const int rr = (i * 32 + lane) / PER, piece = (i * 32 + lane) % PER, lr = l_first + rr;
+                const int64_t at = __shfl_sync(0xffffffffu, off, rr);
+                const uint32_t dst = sbase + q * C::Q_TILE_BYTES + (piece >> 3) * C::Q_CHUNK_BYTES + lr * 128 +
+                                     (((piece & 7) ^ (lr & 7)) << 4);
+                load16(dst, p.q + at + piece * 8, r_first + rr < p.rows);
+            }
+        };
+        // The page of 16-key group `lane` of this warp's share of tile kt.
+        const int page_of_lane = (half * C::COLS + lane % (C::COLS / 16) * 16) >> p.block_shift;
+        constexpr uint32_t kAllPages = (1u << (C::COLS / 16)) - 1;
+        auto load_id = [&](int kt) -> int {
+            const int idx = ((kt * C::BN) >> p.block_shift) + page_of_lane;
+            return idx < p.prefix_blocks ? p.prefix_table[idx] : -1;
+        };
+
+        bool more = ok && walk.next(p, pc);
+        bool q_loading = false;  // pc's Q is on its way
+        while (ok && more) {
             const int base_pos = pos;
             pos += 2 * C::SUB * pc.n;
-            if (q >= pc.tiles) continue;
+            if (q >= pc.tiles) {
+                more = walk.next(p, pc);
+                continue;
+            }
+            if (pc.n > 0 && !q_loading) load_q(pc);
+            q_loading = false;
             const int r = pc.row0 + q * 128 + row;
             int jlo = pc.lo, jhi = P - 1;  // keys of the prefix that the row sees (unused rows: all)
             if (r < p.rows) {
@@ -425,78 +476,66 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                 home = p.pre_cont + tile * (128 * C::D);
                 ml = p.pre_cont_ml + tile * 128;
             }
-            if (pc.n > 0) {
-                // Q rows into shared memory, 128-byte swizzled: a warp its own 32 rows.
-                {
-                    constexpr int PER = C::D / 8;  // 16-byte pieces of a row
-                    const int r_first = pc.row0 + q * 128 + (warp & 3) * 32;
-#pragma unroll 8
-                    for (int i = lane; i < 32 * PER; i += 32) {
-                        const int rr = i / PER, c = i % PER;
-                        const int g_row = r_first + rr;
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (g_row < p.rows) {
-                            const int t = g_row / p.G;
-                            x = *reinterpret_cast<const uint4*>(
-                                p.q + (static_cast<int64_t>(t) * p.Hq + pc.h * p.G + (g_row - t * p.G)) * C::D + c * 8);
-                        }
-                        const int lr = (warp & 3) * 32 + rr;
-                        st_shared_v4(sbase + q * C::Q_TILE_BYTES + (c >> 3) * C::Q_CHUNK_BYTES + lr * 128 +
-                                         (((c & 7) ^ (lr & 7)) << 4),
-                                     x.x, x.y, x.z, x.w);
-                    }
-                    fence_proxy_async_smem();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::B_Q_FULL + q));
-                }
-                // Bit i: the 16-key group i of tile kt lies in a page of the cache.
-                auto load_id = [&](int kt) -> int {
-                    const int idx = ((kt * C::BN) >> p.block_shift) + valid_pages_lane;
-                    return lane < 8 && idx < p.prefix_blocks ? p.prefix_table[idx] : -1;
-                };
+            PrefixPiece next = pc;
+            const int n = pc.n;
+            if (n > 0) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_Q_FULL + q));
                 int id = load_id(pc.kt);
-                for (int j = 0; j < pc.n; ++j) {
+                for (int j = 0; j < n; ++j) {
                     const int t = done + j;
                     const int b = t % C::NSB;
-                    const int key0 = (pc.kt + j) * C::BN;
-                    const uint32_t pages =
-                        __ballot_sync(0xffffffffu, lane < 8 && id >= 0 && id < p.num_blocks) & 0xffu;
-                    if (j + 1 < pc.n) id = load_id(pc.kt + j + 1);
+                    const int key0 = (pc.kt + j) * C::BN + half * C::COLS;  // this warp's first key
+                    const uint32_t pages = __ballot_sync(0xffffffffu, id >= 0 && id < p.num_blocks) & kAllPages;
+                    if (j + 1 < n) id = load_id(pc.kt + j + 1);
                     ok = warp_wait(bar(C::B_S_FULL + q * C::NSB + b), (t / C::NSB) & 1, abort_flag, status);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t s_tmem = lane_base + (q * C::NSB + b) * C::BN;
-                    const bool all = __all_sync(0xffffffffu, key0 >= jlo && key0 + C::BN - 1 <= jhi) && pages == 0xffu;
-                    const int c_lo = jlo > key0 ? (jlo - key0 < C::BN ? jlo - key0 : C::BN) : 0;
-                    const int c_hi = jhi - key0;
-                    // Scores of columns [c0, c0 + 32); hidden ones become -inf.
-                    uint32_t raw[64];
-                    float sv[64];
-                    auto load64 = [&](int c0) {
-                        tmem_ld32(s_tmem + c0, *reinterpret_cast<uint32_t(*)[32]>(&raw[0]));
-                        tmem_ld32(s_tmem + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[32]));
+                    if (j == n - 1) {
+                        // All products with this Q are done: the next piece's may come.
+                        more = walk.next(p, next);
+                        if (more && next.n > 0 && q < next.tiles) {
+                            load_q(next);
+                            q_loading = true;
+                        }
+                    }
+                    const uint32_t s_tmem = s_tmem0 + b * C::BN;
+                    const bool all = __all_sync(0xffffffffu, key0 >= jlo && key0 + C::COLS - 1 <= jhi) && pages == kAllPages;
+                    // Scores of columns [c0, c0 + CK); hidden ones become -inf.
+                    float sv[C::CK];
+                    auto load = [&](int c0) {
+                        uint32_t raw[C::CK];
+#pragma unroll
+                        for (int c = 0; c < C::CK; c += 32) tmem_ld32(s_tmem + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(&raw[c]));
                         tmem_wait_ld();
-                        reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&raw[0]));
-                        reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&raw[32]));
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(raw[c]);
+                        for (int c = 0; c < C::CK; c += 32) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&raw[c]));
+#pragma unroll
+                        for (int c = 0; c < C::CK; ++c) sv[c] = __uint_as_float(raw[c]);
                         if (!all) {
+                            const int at = key0 + c0;
 #pragma unroll
-                            for (int c = 0; c < 64; ++c)
-                                if (c0 + c < c_lo || c0 + c > c_hi || !((pages >> ((c0 + c) >> 4)) & 1u)) sv[c] = -INFINITY;
+                            for (int c = 0; c < C::CK; ++c)
+                                if (at + c < jlo || at + c > jhi || !((pages >> ((c0 + c) >> 4)) & 1u)) sv[c] = -INFINITY;
                         }
                     };
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    auto max64 = [&]() {
+                    auto largest = [&]() -> float {
+                        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-                        for (int c = 0; c < 64; c += 2) mx[(c >> 1) & 3] = max3f(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
+                        for (int c = 4; c < C::CK; c += 2) mx[(c >> 1) & 3] = max3f(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
+                        return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     };
-                    load64(0);
-                    max64();
-                    load64(64);
-                    max64();
-                    const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                    load(0);
+                    float m_tile = largest();
+                    load(C::CK);
+                    m_tile = fmaxf(m_tile, largest()) * sl2;
+                    if constexpr (C::HALVES > 1) {
+                        m_tile = fmaxf(m_tile, swap(m_tile));
+                        if (!ok) break;
+                    }
 
                     float alpha = 1.0f;
                     bool rescale = false;
@@ -516,22 +555,27 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                         if (!ok) break;
                         tc_fence_after();
                     }
-                    // Values of keys that no row of the group sees may be anything:
-                    // zero them, as 0 * NaN would stay NaN.  (Whatever held V(j)'s slots
-                    // before has been consumed by now, so their phase is this one's.)
-                    if (key0 < pc.lo || key0 + C::BN > P) {
-                        const int v_tiles = min(pc.n, C::NSB + j) + j;  // K and V tiles before V(j)
+                    // Values of keys that no row of the group sees may be anything: zero
+                    // them, as 0 * NaN would stay NaN.  (Whatever held V(j)'s slots before
+                    // has been consumed by now, so their phase is this one's.)
+                    if (key0 < pc.lo || key0 + C::COLS > P) {
+                        const int v_tiles = min(n, C::NSB + j) + j;  // K and V tiles before V(j)
 #pragma unroll 1
                         for (int s = 0; s < C::SUB && ok; ++s) {
                             const int at = base_pos + C::SUB * v_tiles + s;
                             ok = warp_wait(bar(C::B_SLOT_FULL + at % C::NSLOT), (at / C::NSLOT) & 1, abort_flag, status);
                             if (!ok) break;
-                            if (key0 + row < pc.lo || key0 + row >= P) {
-                                const uint32_t dst = sbase + C::SMEM_SLOTS + (at % C::NSLOT) * C::SLOT_BYTES + (row >> 3) * C::GROUP_BYTES + (row & 7) * 128;
+                            // (every warp all keys of its share, so that none waits for another)
+#pragma unroll 1
+                            for (int k = lane; k < C::COLS; k += 32) {
+                                if (key0 + k >= pc.lo && key0 + k < P) continue;
+                                const int kr = half * C::COLS + k;
+                                const uint32_t dst = sbase + C::SMEM_SLOTS + (at % C::NSLOT) * C::SLOT_BYTES +
+                                                     (kr >> 3) * C::GROUP_BYTES + (kr & 7) * 128;
+#pragma unroll
                                 for (int c = 0; c < C::CH; ++c)
 #pragma unroll
-                                    for (int u = 0; u < 8; ++u)
-                                        st_shared_v4(dst + c * 1024 + u * 16, 0, 0, 0, 0);
+                                    for (int u = 0; u < 8; ++u) st_shared_v4(dst + c * 1024 + u * 16, 0, 0, 0, 0);
                             }
                         }
                         if (!ok) break;
@@ -539,7 +583,7 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                     }
                     if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-                        for (int c = 0; c < C::D / 32; ++c) {
+                        for (int c = 0; c < O_COLS / 32; ++c) {
                             uint32_t o[32];
                             tmem_ld32(o_tmem + c * 32, o);
                             tmem_wait_ld();
@@ -553,41 +597,51 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                     const float2 sl2x2 = make_float2(sl2, sl2);
                     const float2 negm2 = make_float2(neg_m, neg_m);
                     float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-                    // P of keys 64.. over the score columns [64, 96), which are in registers.
-                    exp_and_store_p<0, 2, 64, 0>(sv, sl2x2, negm2, s_tmem + 64, acc0, acc1);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::B_P_FULL + 2 * q + 1));
-                    load64(0);
-                    exp_and_store_p<0, 2, 64, 0>(sv, sl2x2, negm2, s_tmem, acc0, acc1);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::B_P_FULL + 2 * q));
+                    // P of CK keys over the first half of their score columns: the second chunk
+                    // is still in registers, the first is read again (holding both would
+                    // spill).
+                    auto publish = [&](int i) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::B_P_FULL + 2 * q + i));
+                    };
+                    exp_and_store_p<0, C::CK / 32, C::CK, 0>(sv, sl2x2, negm2, s_tmem + C::CK, acc0, acc1);
+                    if constexpr (C::HALVES == 1) publish(1);
+                    load(0);
+                    exp_and_store_p<0, C::CK / 32, C::CK, 0>(sv, sl2x2, negm2, s_tmem, acc0, acc1);
+                    publish(half);
                     l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
                 }
                 if (ok)
-                    ok = warp_wait(bar(C::B_O_FULL + q), C::NSB == 1 ? pieces & 1 : (done + pc.n - 1) & 1, abort_flag,
-                                   status);
+                    ok = warp_wait(bar(C::B_O_FULL + q), C::NSB == 1 ? pieces & 1 : (done + n - 1) & 1, abort_flag, status);
                 if (!ok) break;
+                if constexpr (C::HALVES > 1) {
+                    l += swap(l);
+                    if (!ok) break;
+                }
                 tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < C::D / 32; ++c) {
+                for (int c = 0; c < O_COLS / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld32(o_tmem + c * 32, o);
                     tmem_wait_ld();
                     reg_fence32(o);
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
-                        *reinterpret_cast<uint4*>(home + ((c * 8 + u) * 128 + row) * 4) =
+                        *reinterpret_cast<uint4*>(home + ((half * (O_COLS / 4) + c * 8 + u) * 128 + row) * 4) =
                             make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
                 }
                 ++pieces;
-                done += pc.n;
+                done += n;
+            } else {
+                more = walk.next(p, next);
             }
-            ml[row] = make_float2(m_ref, l);
+            if (half == 0) ml[row] = make_float2(m_ref, l);
+            pc = next;
         }
+        if (C::HALVES > 1 && !ok) asm volatile("bar.arrive %0, 64;" ::"r"(pair_bar) : "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
 
     tc_fence_before();
