@@ -37,6 +37,18 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
+// The same for data that is read once: L2 gives it up first, before the prefix's
+// keys and the parts that the merge kernel reads.
+__device__ __forceinline__ uint64_t read_once_policy() {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+__device__ __forceinline__ void load16_once(uint32_t dst, const void* src, bool there, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0), "l"(policy) : "memory");
+}
+
 // Arrives on the barrier when this thread's loads so far have landed.
 __device__ __forceinline__ void loads_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -309,6 +321,7 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
         constexpr float kTau = 8.0f;  // rescale only when a maximum grows by more than 2^8
         const uint32_t ring = sbase + wk * (C::NSLOT * C::SLOT_BYTES);
         const int full0 = C::B_FULL + wk * C::NSLOT, empty0 = C::B_EMPTY + wk * C::NSLOT;
+        const uint64_t once = read_once_policy();
         int pos = 0, issued = 0;  // ring positions read and loaded
         bool ok = *abort_flag == 0;
         PagedPiece pc;
@@ -359,8 +372,8 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
 #pragma unroll
                     for (int i = 0; i < 16 / STEP; ++i) {
                         const int rr = part * 16 + i * STEP;  // + row: the row in the slice
-                        load16(dst + rr * C::ROW_BYTES + (((lane % LANES) ^ ((rr + row) & 7)) << 4), src + (id >= 0 ? i * step : 0),
-                               id >= 0);
+                        load16_once(dst + rr * C::ROW_BYTES + (((lane % LANES) ^ ((rr + row) & 7)) << 4),
+                                    src + (id >= 0 ? i * step : 0), id >= 0, once);
                     }
                 }
                 loads_arrive(bar(full0 + slot));
