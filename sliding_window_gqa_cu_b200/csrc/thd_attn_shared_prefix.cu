@@ -7,8 +7,8 @@
 //
 // Three launches, overlapped by programmatic dependent launch:
 //   thd_sp_prefix_kernel  the shared prefix, once for all rows (tensor cores)
-//   thd_sp_paged_kernel   each request's own pages (bound by memory); it starts
-//                         while the prefix kernel runs and shares its SMs
+//   thd_sp_paged_kernel   each request's own pages (bound by memory); it runs
+//                         on the SMs that the prefix kernel leaves
 //   thd_sp_merge_kernel   adds the parts and the sinks, divides, writes
 // With few rows in all (one row tile of the paged kernel) that kernel takes the
 // prefix as well and the first launch falls away.
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(512) thd_sp_merge_kernel(const SpParams p) {
         const int64_t bh = static_cast<int64_t>(b) * p.Hkv + h;
         const int pre_item = r / p.pg_rows * p.Hkv + h;
         const int n = thd::sp_own_len(p, b);
-        thd::SpPlan plan{0, 0, 0};
+        thd::SpPlan plan{0, 0, 0, 0};
         long long begin = 0;  // (means nothing for an item without keys)
         if (p.any_keys) {
             plan = *p.plan;
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(512) thd_sp_merge_kernel(const SpParams p) {
             const int tile = r >> 7, group = tile / NT, q = tile - group * NT, row = r & 127;
             const int len = plan.pre_tiles + thd::kItemTiles;
             units = static_cast<long long>((p.pre_groups + p.pre_width - 1) / p.pre_width) * p.Hkv * len;
-            lanes = thd::sp_prefix_lanes(p, units);
+            lanes = plan.pre_lanes;
             x = (static_cast<long long>(group / p.pre_width) * p.Hkv + h) * len + thd::kItemTiles;
             step = p.pre_width;
             member = group % p.pre_width;

@@ -38,6 +38,7 @@ struct SpPlan {
     long long pg_units;
     int pg_lanes;
     int pre_tiles;  // key tiles (paged kernel: slices) of the prefix
+    int pre_lanes;
 };
 
 struct SpParams {
@@ -106,10 +107,10 @@ __device__ __forceinline__ int lane_of(long long units, int lanes, long long x) 
     return static_cast<int>(at / static_cast<unsigned long long>(units));
 }
 
-// Lanes that the prefix kernel's units are cut over: some units each (parts of
-// fewer tiles would cost more traffic than they share out).
+// Lanes that the prefix kernel's units are cut over at most: three units each (a part costs
+// the traffic of two to four tiles).
 __device__ __forceinline__ int sp_prefix_lanes(const SpParams& p, long long units) {
-    return static_cast<int>(min((units + kItemTiles + 1) / (kItemTiles + 2), static_cast<long long>(p.pre_lanes)));
+    return static_cast<int>(min((units + 2) / 3, static_cast<long long>(p.pre_lanes)));
 }
 
 __device__ __forceinline__ int sp_prefix_len(const SpParams& p) {
@@ -138,6 +139,55 @@ __device__ __forceinline__ int sp_first_own(const SpParams& p, int n) {
 template <int KS>
 __device__ __forceinline__ int sp_own_slices(const SpParams& p, int n) {
     return n > 0 ? (n - 1) / KS + 1 - sp_first_own(p, n) / KS : 0;
+}
+
+// Units of the prefix kernel for n_tiles key tiles.
+__device__ __forceinline__ long long sp_prefix_units(const SpParams& p, int n_tiles) {
+    if (n_tiles <= 0) return 0;
+    return static_cast<long long>((p.pre_groups + p.pre_width - 1) / p.pre_width) * p.Hkv * (n_tiles + kItemTiles);
+}
+
+struct SpSplit {
+    int lanes;  // of the prefix kernel that work
+    int free;   // SMs that it leaves to the paged kernel
+};
+
+// How the two kernels share the SMs: the prefix kernel is bound by its chain of
+// products and softmax, the paged kernel by memory, which half of the SMs can
+// keep busy, so both run side by side and the choice that ends the later one
+// soonest is taken.  The prefix takes kStart + tile * units / lanes; the requests'
+// own keys kStartPaged + bytes at kSmRate per SM, kMemRate at most (ns, and bytes
+// a ns, as measured).  Every thread has its own candidates; the best of the warp
+// wins.  64 requests on 8,191 tokens 92 us one after the other, 78 side by side,
+// 256 on 32,768 474 and 393; both kernels' CTAs on the same SM 96 and 638 (the
+// softmax warps lose more by waiting for issue slots and loads than memory gains).
+template <int D>
+__device__ __forceinline__ SpSplit sp_split(const SpParams& p, long long units, float own_keys) {
+    constexpr float kMemRate = 5000.0f, kSmRate = 80.0f, kStart = 10000.0f, kStartPaged = 12000.0f;
+    constexpr float kTile = D == 64 ? 1600.0f : 2300.0f;
+    const float bytes = own_keys * p.Hkv * (D * 4);
+    const int most = units > 0 ? sp_prefix_lanes(p, units) : 0;
+    float best = INFINITY;
+    int lanes = most;
+    for (int l = 1 + static_cast<int>(threadIdx.x & 31); l <= most; l += 32) {
+        const float prefix = kStart + kTile * (static_cast<float>(units) / l);
+        const float rate = fminf(kMemRate, (kSpLanes - l * p.pre_width) * kSmRate);
+        const float time = bytes > 0.0f ? fmaxf(prefix, kStartPaged + bytes / rate) : prefix;
+        if (time <= best) {
+            best = time;
+            lanes = l;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, best, o);
+        const int l = __shfl_xor_sync(0xffffffffu, lanes, o);
+        if (other < best || (other == best && l > lanes)) {
+            best = other;
+            lanes = l;
+        }
+    }
+    return SpSplit{lanes, kSpLanes - lanes * p.pre_width};
 }
 
 }  // namespace thd

@@ -237,12 +237,15 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
             return n > 0 ? static_cast<long long>(sp_own_slices<C::KS>(p, n) + kItemUnits) * unit : 0;
         };
         int least = 0x7fffffff, longest = 0;  // own length; slices of an item
+        float keys = 0.0f;
         long long mine = 0;
         for (int b = b0; b < b1; ++b) {
             const int n = sp_own_len(p, b);
             mine += units_of(n);
             if (n >= 0) least = min(least, n);
-            if (n > 0) longest = max(longest, sp_own_slices<C::KS>(p, n));
+            if (n <= 0) continue;
+            longest = max(longest, sp_own_slices<C::KS>(p, n));
+            keys += static_cast<float>(n - sp_first_own(p, n));
         }
         long long incl = mine;
 #pragma unroll
@@ -252,10 +255,15 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
         }
         least = __reduce_min_sync(0xffffffffu, least);
         longest = __reduce_max_sync(0xffffffffu, longest);
+        float* keys_of = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
         if (lane == 31) start[warp] = incl;
+        if (lane == 0) keys_of[warp] = keys;
         if (lane == 0) start[4 + warp] = static_cast<long long>(longest) << 32 | least;
         __syncthreads();
         long long before = incl - mine, total = 0;
+        keys = keys_of[0] + keys_of[1] + keys_of[2] + keys_of[3];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             if (w < warp) before += start[w];
@@ -272,14 +280,17 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
                              ? static_cast<long long>(p.pg_prefix) * p.Hkv * (walk.pre_slices + kItemUnits) : 0;
         const long long units = walk.pre_units + total;
         // Units that a worker gets at least.  A part more costs its traffic (written
-        // and read, 2 ROWS / KS slices' worth: a quarter of the slices' at most) and,
-        // for the item with most parts, time in the merge kernel: some 0.15 us a part
-        // against 0.7 us a slice here, so the time of u units and longest / u parts is
-        // least near the root of longest / 5.
+        // and read, 2 ROWS / KS slices' worth) and, for the item with most parts, time in
+        // the merge kernel: some 0.15 us a part against 0.7 us a slice here, so the time
+        // of u units and longest / u parts is least near the root of longest / 5.
         longest = max(longest, walk.pre_slices);
-        const int least_units = max(max(4, 8 * C::ROWS / C::KS), static_cast<int>(sqrtf(0.2f * longest)));
+        const int least_units = max(max(4, 2 * C::ROWS / C::KS), static_cast<int>(sqrtf(0.2f * longest)));
+        // One wave of CTAs on the SMs that the prefix kernel leaves.
+        int ctas = p.pg_ctas;
+        if (p.pre_lanes > 0 && lo < P)
+            ctas = min(ctas, C::RESIDENT * max(1, sp_split<C::D>(p, sp_prefix_units(p, (P - 1) / 128 + 1 - lo / 128), keys).free));
         const int lanes = static_cast<int>(min((units + least_units - 1) / least_units,
-                                               static_cast<long long>(p.pg_ctas) * C::WORKERS));
+                                               static_cast<long long>(ctas) * C::WORKERS));
         // Where each worker's range begins among the own units.
 #pragma unroll
         for (int i = 0; i < C::WORKERS; ++i) {

@@ -13,7 +13,8 @@
 // Work split: groups of NT * 128 rows; `pre_width` groups of a kv head walk the
 // same keys in step (one CTA each, so that K and V come from L2 for all but the
 // first), and the sequence (bundle of groups, kv head, key tile) is cut into
-// equal ranges, one per lane of CTAs.
+// equal ranges, one per lane of CTAs.  How many lanes work is decided from the
+// lengths (sp_split): the CTAs beyond leave their SMs to the paged kernel.
 //
 // Warps: 8 softmax warps (a thread a row; D = 256: two), a TMA producer for K and
 // one for V, an MMA issuer.  A TMA box holds a page's tokens (128 at most) x all
@@ -63,7 +64,7 @@ struct PrefixConfig {
 
     static constexpr int SMEM_SLOTS = NT * Q_TILE_BYTES;
     static constexpr int SMEM_BAR = SMEM_SLOTS + NSLOT * SLOT_BYTES;
-    static constexpr int SMEM_MIN = SMEM_BAR + NUM_BARS * 8;  // [warp]: least own length
+    static constexpr int SMEM_MIN = SMEM_BAR + NUM_BARS * 8;  // [2][16]: least own length, own keys of a warp's requests
     static constexpr int SMEM_XCH = SMEM_MIN + 32 * 4;          // float [NSB][NT][2][128]: maxima (sums) of two threads of a row
     static constexpr int SMEM_TMEM_SLOT = SMEM_XCH + (HALVES > 1 ? NSB * NT * 2 * 128 * 4 : 0);
     static constexpr int SMEM_ABORT = SMEM_TMEM_SLOT + 4;
@@ -139,6 +140,7 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::SMEM_ABORT);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SMEM_TMEM_SLOT);
     int* warp_min = reinterpret_cast<int*>(smem + C::SMEM_MIN);
+    float* warp_keys = reinterpret_cast<float*>(warp_min + 16);
 
     if (threadIdx.x == 0) {
         for (int q = 0; q < C::NT; ++q) {
@@ -165,17 +167,24 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         tmem_alloc(smem_addr(tmem_slot), 512);
         tmem_relinquish();
     }
-    // Key tiles that any row can see.
+    // Least own length (for the first key that any row sees) and all own keys.
     const int P = sp_prefix_len(p);
     {
         int n = 0x7fffffff;
-        if (p.window > 0)
-            for (int b = threadIdx.x; b < p.n_req; b += C::THREADS) {
-                const int len = sp_own_len(p, b);
-                if (len >= 0) n = min(n, len);
-            }
+        float keys = 0.0f;
+        for (int b = threadIdx.x; b < p.n_req; b += C::THREADS) {
+            const int len = sp_own_len(p, b);
+            if (len < 0) continue;
+            n = min(n, len);
+            keys += static_cast<float>(len - sp_first_own(p, len));
+        }
         n = __reduce_min_sync(0xffffffffu, n);
-        if (lane == 0) warp_min[warp] = n;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
+        if (lane == 0) {
+            warp_min[warp] = n;
+            warp_keys[warp] = keys;
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -185,23 +194,26 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
 
     PrefixWalk<C> walk;
     {
-        int lo = 0;
-        if (p.window > 0) {
-            int n = 0x7fffffff;
-            for (int w = 0; w < C::THREADS / 32; ++w) n = min(n, warp_min[w]);
-            lo = n == 0x7fffffff ? P : sp_first_key(p, P + n - p.n_q);
+        int n = 0x7fffffff;
+        float keys = 0.0f;
+        for (int w = 0; w < C::THREADS / 32; ++w) {
+            n = min(n, warp_min[w]);
+            keys += warp_keys[w];
         }
+        const int lo = n == 0x7fffffff ? P : sp_first_key(p, P + n - p.n_q);
         walk.first_tile = lo / C::BN;
         walk.n_tiles = lo < P ? (P - 1) / C::BN + 1 - walk.first_tile : 0;
         walk.prefix = P;
         walk.member = blockIdx.x % p.pre_width;
         const int my_lane = blockIdx.x / p.pre_width;
-        const long long units = static_cast<long long>((p.pre_groups + p.pre_width - 1) / p.pre_width) * p.Hkv *
-                                (walk.n_tiles > 0 ? walk.n_tiles + kItemTiles : 0);
-        const int lanes = sp_prefix_lanes(p, units);
+        const long long units = sp_prefix_units(p, walk.n_tiles);
+        const int lanes = sp_split<C::D>(p, units, keys).lanes;
         walk.x = my_lane < lanes ? lane_begin(units, lanes, my_lane) : 0;
         walk.x1 = my_lane < lanes ? lane_begin(units, lanes, my_lane + 1) : 0;
-        if (blockIdx.x == 0 && threadIdx.x == 0) p.plan->pre_tiles = walk.n_tiles;
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            p.plan->pre_tiles = walk.n_tiles;
+            p.plan->pre_lanes = lanes;
+        }
     }
     PrefixPiece pc;
 
