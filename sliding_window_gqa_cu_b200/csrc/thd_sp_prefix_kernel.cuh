@@ -17,7 +17,7 @@
 // lengths (sp_split): the CTAs beyond leave their SMs to the paged kernel.
 //
 // Warps: 8 softmax warps (a thread a row; D = 256: two), a TMA producer for K and
-// one for V, an MMA issuer.  A TMA box holds a page's tokens (128 at most) x all
+// one for V, an MMA issuer for each row tile.  A TMA box holds a page's tokens (128 at most) x all
 // columns of a slot: [tokens / 8][column chunk][8 tokens][64 columns], whose
 // groups of 8 tokens have one stride over the pages of a tile, as the matrix
 // descriptors need it.
@@ -49,7 +49,7 @@ struct PrefixConfig {
     static constexpr int K_WARP = SOFTMAX_WARPS;
     static constexpr int V_WARP = SOFTMAX_WARPS + 1;
     static constexpr int MMA_WARP = SOFTMAX_WARPS + 2;
-    static constexpr int THREADS = (SOFTMAX_WARPS + 3) * 32;
+    static constexpr int THREADS = (SOFTMAX_WARPS + 2 + NT) * 32;
     static constexpr int TMEM_O = NT * NSB * BN;
     static_assert(TMEM_O + NT * D <= 512, "TMEM budget exceeded");
 
@@ -59,7 +59,8 @@ struct PrefixConfig {
     static constexpr int B_S_FULL = B_SLOT_EMPTY + NSLOT;     // [NT][NSB]
     static constexpr int B_P_FULL = B_S_FULL + NT * NSB;      // [NT][2]: P of 64 keys written, O rescaled
     static constexpr int B_O_FULL = B_P_FULL + 2 * NT;        // [NT]
-    static constexpr int B_DRAIN = B_O_FULL + NT;
+    static constexpr int B_TURN = B_O_FULL + NT;              // [NT]
+    static constexpr int B_DRAIN = B_TURN + NT;
     static constexpr int NUM_BARS = B_DRAIN + 1;
 
     static constexpr int SMEM_SLOTS = NT * Q_TILE_BYTES;
@@ -126,6 +127,13 @@ struct PrefixWalk {
     }
 };
 
+// Wait of a whole warp, every thread polling: the shortest way if the phase is
+// over already.
+__device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return warp_wait(bar, parity, abort_flag, status);
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
 thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -151,10 +159,11 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         }
         for (int s = 0; s < C::NSLOT; ++s) {
             mbar_init(bar(C::B_SLOT_FULL + s), 1);
-            mbar_init(bar(C::B_SLOT_EMPTY + s), 1);
+            mbar_init(bar(C::B_SLOT_EMPTY + s), C::NT);
         }
         for (int i = 0; i < C::NT * C::NSB; ++i) mbar_init(bar(C::B_S_FULL + i), 1);
-        mbar_init(bar(C::B_DRAIN), 1);
+        for (int q = 0; q < C::NT; ++q) mbar_init(bar(C::B_TURN + q), 1);
+        mbar_init(bar(C::B_DRAIN), C::NT);
         int bad = *reinterpret_cast<volatile int*>(status) != 0 ? 1 : 0;
         if ((sbase & 1023u) != 0) {  // the swizzled tiles need it
             atomicCAS(status, 0, kStatusBadItem);
@@ -274,19 +283,26 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                         drain_wait(bar(C::B_SLOT_FULL + (pos - 1 - i) % C::NSLOT), ((pos - 1 - i) / C::NSLOT) & 1);
         }
         __syncwarp();
-    } else if (warp == C::MMA_WARP) {
-        // -------------------------------------------------------- MMA issuer
+    } else if (warp >= C::MMA_WARP && warp < C::MMA_WARP + C::NT) {
+        // ------------------------------------------ MMA issuers, one a row tile
+        // Issuing is what one warp for both row tiles spends its time on: 32 instructions
+        // (about 52 cycles each), six waits (some 200) and four commits, 4,000 cycles a
+        // pair of tiles, where the products need 2,048.  One warp a tile: 256 requests on
+        // 32,768 tokens 256 -> 250 us, 64 on 8,191 38 -> 33 us for this kernel.
         if (!skip) {
+            const int q = warp - C::MMA_WARP;
+            const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, C::BN, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, C::SC, true);
             const uint64_t dq0 = smem_desc_sw128(sbase, 16, 1024);
             const uint64_t dk0 = smem_desc_sw128(sbase + C::SMEM_SLOTS, 16, C::GROUP_BYTES);
             const uint64_t dv0 = smem_desc_sw128(sbase + C::SMEM_SLOTS, 1024, C::GROUP_BYTES);
             // Part s of S = Q K^T: head-dim columns [s SC, (s + 1) SC).
-            auto issue_qk = [&](int q, int b, int s, int slot) {
+            auto issue_qk = [&](int b, int s, int slot) {
                 const uint32_t d_tmem = tmem_base + (q * C::NSB + b) * C::BN;
                 const uint64_t dq = dq0 + ((q * C::Q_TILE_BYTES + s * C::CH * C::Q_CHUNK_BYTES) >> 4);
                 const uint64_t dk = dk0 + ((slot * C::SLOT_BYTES) >> 4);
+                if (!elect_one()) return;
 #pragma unroll
                 for (int kk = 0; kk < C::SC / 16; ++kk) {
                     const uint32_t qo = ((kk >> 2) * C::Q_CHUNK_BYTES + (kk & 3) * 32) >> 4;
@@ -296,107 +312,108 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             };
             // Part s of O += P V (columns [s SC, ..)) over keys [64 half, 64 half + 64),
             // whose P lies in the first half of every CK score columns.
-            auto issue_pv = [&](int q, int b, int s, int slot, int half, bool acc) {
+            auto issue_pv = [&](int b, int s, int slot, int half, bool acc) {
                 const uint32_t d_tmem = tmem_base + C::TMEM_O + q * C::D + s * C::SC;
                 const uint32_t p_tmem = tmem_base + (q * C::NSB + b) * C::BN + half * 64;
                 const uint64_t dv = dv0 + ((slot * C::SLOT_BYTES + half * 8 * C::GROUP_BYTES) >> 4);
+                if (!elect_one()) return;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_bf16_ts(d_tmem, p_tmem + kk * 16 / C::CK * C::CK + kk * 16 % C::CK / 2, dv + ((kk * 2 * C::GROUP_BYTES) >> 4), idesc_pv,
                                 acc || kk > 0 ? 1u : 0u);
             };
-            int pos = 0, pieces[2] = {0, 0}, done[2] = {0, 0};  // per row tile
+            auto commit = [&](int idx) {
+                if (elect_one()) mma_commit(bar(idx));
+            };
+            int pos = 0, pieces = 0, done = 0, turns = 0;
             bool ok = true;
             auto wait = [&](int idx, uint32_t parity) -> bool {
-                return mbar_wait(bar(idx), parity, abort_flag, status, kStatusTimeout);
+                return warp_poll(bar(idx), parity, abort_flag, status);
             };
             auto wait_slot = [&](int at) -> bool {
                 return wait(C::B_SLOT_FULL + at % C::NSLOT, (at / C::NSLOT) & 1);
             };
             while (walk.next(p, pc)) {
                 if (pc.n == 0 || !ok) continue;
-                if (lane == 0) {
-                    const int n = pc.n;
-                    for (int q = 0; q < pc.tiles && ok; ++q) ok = wait(C::B_Q_FULL + q, pieces[q] & 1);
-                    // K tile of step jj at ring position `pos`: one part per slot
-                    auto qk = [&](int jj) {
-                        for (int s = 0; s < C::SUB && ok; ++s) {
-                            ok = wait_slot(pos + s);
-                            if (!ok) return;
-                            tc_fence_after();
-                            for (int q = 0; q < pc.tiles; ++q)
-                                issue_qk(q, (done[q] + jj) % C::NSB, s, (pos + s) % C::NSLOT);
-                            if (s == C::SUB - 1)
-                                for (int q = 0; q < pc.tiles; ++q)
-                                    mma_commit(bar(C::B_S_FULL + q * C::NSB + (done[q] + jj) % C::NSB));
-                            mma_commit(bar(C::B_SLOT_EMPTY + (pos + s) % C::NSLOT));
-                        }
-                    };
-                    for (int jj = 0; jj < C::NSB && jj < n && ok; ++jj) {
-                        qk(jj);
-                        pos += C::SUB;
+                const int n = pc.n;
+                if (q >= pc.tiles) {
+                    // No rows in this tile: its share of the slots' releases only.
+                    for (int i = 0; i < 2 * n * C::SUB && ok; ++i, ++pos) {
+                        ok = wait_slot(pos);
+                        if (ok && lane == 0) mbar_arrive(bar(C::B_SLOT_EMPTY + pos % C::NSLOT));
                     }
-                    for (int j = 0; j < n && ok; ++j) {
-                        const bool more = j + C::NSB < n;
-                        const int vpos = pos, kpos = pos + C::SUB;
-                        if constexpr (C::NSB == 1) {
-                            // PV(j) and QK(j + 1) of a row tile go out as one run with one
-                            // commit: S(j + 1) ready also says that O holds PV(j).
-                            ok = wait_slot(vpos);
-                            for (int q = 0; q < pc.tiles && ok; ++q) {
-                                // (the second chunk is published first)
-                                for (int half = 1; half >= 0 && ok; --half) {
-                                    ok = wait(C::B_P_FULL + 2 * q + half, (done[q] + j) & 1);
-                                    if (!ok) break;
-                                    tc_fence_after();
-                                    issue_pv(q, 0, 0, vpos % C::NSLOT, half, j > 0 || half == 0);
-                                }
-                                if (!ok) break;
-                                if (more) {
-                                    if (q == 0) ok = wait_slot(kpos);
-                                    if (!ok) break;
-                                    tc_fence_after();
-                                    issue_qk(q, 0, 0, kpos % C::NSLOT);
-                                    mma_commit(bar(C::B_S_FULL + q));
-                                } else {
-                                    mma_commit(bar(C::B_O_FULL + q));
-                                }
-                            }
-                            if (!ok) break;
-                            mma_commit(bar(C::B_SLOT_EMPTY + vpos % C::NSLOT));
-                            if (more) mma_commit(bar(C::B_SLOT_EMPTY + kpos % C::NSLOT));
-                            pos += more ? 2 : 1;
-                        } else {
-                            const int b = (done[0] + j) % C::NSB;
-                            for (int half = 0; half < 2 && ok; ++half)
-                                ok = wait(C::B_P_FULL + half, (done[0] + j) & 1);
-                            for (int s = 0; s < C::SUB && ok; ++s) {
-                                ok = wait_slot(vpos + s);
-                                if (!ok) break;
-                                tc_fence_after();
-                                issue_pv(0, b, s, (vpos + s) % C::NSLOT, 0, j > 0);
-                                issue_pv(0, b, s, (vpos + s) % C::NSLOT, 1, true);
-                                if (s == C::SUB - 1) mma_commit(bar(C::B_O_FULL));
-                                mma_commit(bar(C::B_SLOT_EMPTY + (vpos + s) % C::NSLOT));
-                            }
-                            pos += C::SUB;
-                            if (ok && more) {
-                                qk(j + C::NSB);
-                                pos += C::SUB;
-                            }
-                        }
-                    }
-                    for (int q = 0; q < pc.tiles; ++q) {
-                        ++pieces[q];
-                        done[q] += n;
-                    }
+                    continue;
                 }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                ok = wait(C::B_Q_FULL + q, pieces & 1);
+                // K tile of step jj at ring position `pos`: one part per slot
+                auto qk = [&](int jj) {
+                    for (int s = 0; s < C::SUB && ok; ++s, ++pos) {
+                        ok = wait_slot(pos);
+                        if (!ok) return;
+                        tc_fence_after();
+                        issue_qk((done + jj) % C::NSB, s, pos % C::NSLOT);
+                        if (s == C::SUB - 1) commit(C::B_S_FULL + q * C::NSB + (done + jj) % C::NSB);
+                        commit(C::B_SLOT_EMPTY + pos % C::NSLOT);
+                    }
+                };
+                for (int jj = 0; jj < C::NSB && jj < n && ok; ++jj) qk(jj);
+                if (C::NT == 2 && pc.tiles == 2) {
+                    // The row tiles take turns: PV(j) and QK(j + 1) of one go out as one run
+                    // while the other is in its softmax.  (Without turns both tiles drift into
+                    // step, all softmax and then all products: 4,500 cycles a pair of tiles.)
+                    for (int j = 0; j < n && ok; ++j) {
+                        const bool more = j + 1 < n;
+                        // (what is long there is waited for first)
+                        ok = wait_slot(pos) && (!more || wait_slot(pos + 1)) && wait(C::B_P_FULL + 2 * q + 1, (done + j) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(0, 0, pos % C::NSLOT, 1, j > 0);
+                        ok = wait(C::B_P_FULL + 2 * q, (done + j) & 1) && wait(C::B_TURN + q, (turns & 1) ^ (q == 0 ? 1 : 0));
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(0, 0, pos % C::NSLOT, 0, true);
+                        if (more) {
+                            issue_qk(0, 0, (pos + 1) % C::NSLOT);
+                            commit(C::B_S_FULL + q);
+                        } else {
+                            commit(C::B_O_FULL + q);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::B_TURN + 1 - q));
+                        ++turns;
+                        commit(C::B_SLOT_EMPTY + pos % C::NSLOT);
+                        if (more) commit(C::B_SLOT_EMPTY + (pos + 1) % C::NSLOT);
+                        pos += more ? 2 : 1;
+                    }
+                    ++pieces;
+                    done += n;
+                    continue;
+                }
+                for (int j = 0; j < n && ok; ++j) {
+                    const bool more = j + C::NSB < n;
+                    const int b = (done + j) % C::NSB;
+                    // PV(j); with one score buffer S(j + 1) ready also says that O holds it.
+                    for (int s = 0; s < C::SUB && ok; ++s, ++pos) {
+                        ok = wait_slot(pos);
+                        // (with one thread a row its second chunk is published first)
+                        for (int i = 0; i < 2 && ok; ++i) {
+                            const int half = C::HALVES == 1 ? 1 - i : i;
+                            if (s == 0) ok = wait(C::B_P_FULL + 2 * q + half, (done + j) & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_pv(b, s, pos % C::NSLOT, half, j > 0 || i > 0);
+                        }
+                        if (!ok) break;
+                        if (s == C::SUB - 1 && (C::NSB == 2 || !more)) commit(C::B_O_FULL + q);
+                        commit(C::B_SLOT_EMPTY + pos % C::NSLOT);
+                    }
+                    if (ok && more) qk(j + C::NSB);
+                }
+                ++pieces;
+                done += n;
             }
-            if (lane == 0) {
-                mma_commit(bar(C::B_DRAIN));
-                drain_wait(bar(C::B_DRAIN), 0);
-            }
+            if (elect_one()) mma_commit(bar(C::B_DRAIN));
+            if (lane == 0) drain_wait(bar(C::B_DRAIN), 0);
         }
         __syncwarp();
     } else {
