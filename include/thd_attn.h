@@ -470,7 +470,8 @@ int thd_sparse_mla_get_error(void* stream);
  *   refused             int32 [1]: how many requests were refused
  * 1 <= n_req <= 8192 (else THD_ERR_UNSUPPORTED), n_rows >= 0, block_size >= 1,
  * max_blocks >= 1, free_capacity >= 0; all pointers 4-byte aligned.
- * n_req = 0 is a no-op.  Deterministic (no atomics).  One launch.
+ * n_req = 0 is a no-op.  Deterministic (no atomics).  One launch.  Apart from
+ * the arrays that may be the same, outputs must not overlap inputs.
  */
 int thd_kv_block_tables(const int32_t* seq_lens, const int32_t* new_lens, int n_req, int block_size,
                         int32_t* block_tables, int max_blocks,
@@ -536,7 +537,14 @@ int thd_kv_write(const void* k, const void* v, int64_t k_row_stride, int64_t v_r
  * THD_ERR_UNSUPPORTED.  (prefix_blocks + max_blocks) * block_size < 2^31,
  * window >= 0, scale finite and > 0; out of range THD_ERR_INVALID_ARG.
  * n_req = 0 is a no-op.  Kernel stalls are reported by
- * thd_attn_shared_prefix_get_error.
+ * thd_attn_shared_prefix_get_error.  (num_blocks - 1) * block_stride +
+ * (Hkv - 1) * head_stride, in units of the greatest common divisor of the two
+ * strides, has to stay below 2^31 (any pool of whole pages does), else
+ * THD_ERR_UNSUPPORTED.
+ * Up to three launches, the later ones begun early on the same stream
+ * (programmatic dependent launch): what follows on the stream waits for all.
+ * thd_attn_shared_prefix_workspace_bytes returns 0 for sizes that are not
+ * supported; lengths and tables do not change it.
  */
 size_t thd_attn_shared_prefix_workspace_bytes(int n_req, int n_q, int Hq, int Hkv, int D);
 int thd_attn_shared_prefix(const void* q, const void* k_cache, const void* v_cache,

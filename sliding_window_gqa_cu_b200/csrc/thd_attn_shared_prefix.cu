@@ -373,6 +373,8 @@ int launch_all(SpParams p, const Maps& maps, cudaStream_t stream) {
 extern "C" size_t thd_attn_shared_prefix_workspace_bytes(int n_req, int n_q, int Hq, int Hkv, int D) {
     if (n_req <= 0 || n_q <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || D <= 0) return 0;
     if (D != 64 && D != 128 && D != 256) return 0;
+    const int64_t G = Hq / Hkv;
+    if (G > 128 || n_req * ((n_q + 128 / G - 1) / (128 / G)) > kMaxUnits) return 0;
     return make_layout(n_req, n_q, Hq, Hkv, D).bytes;
 }
 

@@ -340,8 +340,9 @@ extern "C" int thd_kv_block_tables(const int32_t* seq_lens, const int32_t* new_l
                 free_capacity, n_rows, n_req, block_size, max_blocks, false};
     int ctas = static_cast<int>(std::clamp<int64_t>(std::max<int64_t>(n_rows / 4096, n_req / 64), 1, kTabCtas));
     if (n_req <= 256 && n_rows <= 4096) ctas = 1;
-    if (seq_lens_out == seq_lens || free_count_out == free_count) ctas = std::min(ctas, kTabCluster);
-    p.cluster = ctas > 1 && (seq_lens_out == seq_lens || free_count_out == free_count);
+    const bool in_place = seq_lens_out == seq_lens || seq_lens_out == new_lens || free_count_out == free_count;
+    if (in_place) ctas = std::min(ctas, kTabCluster);
+    p.cluster = ctas > 1 && in_place;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     const int per = (n_req + kTabThreads - 1) / kTabThreads;
     if (per == 1) return launch_tables<1>(p, ctas, stream);

@@ -110,3 +110,17 @@ def test_cache_layouts():
         strides(c[:1].expand(4, 16, 2, 128), c[:1].expand(4, 16, 2, 128), dev)  # overlapping blocks
     with pytest.raises(ValueError):
         strides(c, c.float(), dev)
+
+
+def test_attend_refuses_places_beyond_32_bits(lib):
+    # blocks whose distance shares no more than 8 elements with the heads': more
+    # places than the tensor map counts (33 rows, so the prefix goes through it)
+    kw = dict(nb=1 << 20, sb=(1 << 20) + 8, pt=PTR, n_pt=4, plen=PTR, n_req=33, Hq=2, Hkv=2)
+    assert _attend(lib, **kw) == -2
+
+
+def test_workspace_of_unsupported_sizes(lib):
+    f = swa.thd_attn_shared_prefix_workspace_bytes
+    assert f(4097, 1, 8, 2, 128) == 0 and f(1 << 20, 1 << 20, 8, 2, 128) == 0 and f(2, 1, 258, 2, 128) == 0
+    assert f(2, 1, 8, 2, 96) == 0 and f(2, 1, 7, 2, 128) == 0
+    assert f(4096, 1, 8, 8, 64) > 0 and f(1, 4096 * 128, 8, 8, 64) > 0

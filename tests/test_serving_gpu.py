@@ -510,3 +510,162 @@ def test_prompt_then_answers_match_the_packed_oracle(window, sinks):
     seq[1] = 0
     step([2, 40, 0, 2], 2)                                 # its pages serve another
     step([1, 1, 0, 1], 1)
+
+
+# --------------------------------- many rows: the prefix on the tensor cores
+
+MANY = [
+    # several row groups and bundles of a kv head; groups that end inside a tile
+    dict(P=700, lens=[1] * 300, n_q=1, Hq=8, Hkv=1, D=64, block=16),
+    dict(P=131, lens=[7, 40] * 65, n_q=2, Hq=10, Hkv=1, D=128, block=32),
+    dict(P=1000, lens=[5] * 33, n_q=1, Hq=16, Hkv=2, D=256, block=16),
+    # long prefixes: every item in many pieces
+    dict(P=9001, lens=[33, 700, 1] * 4, n_q=1, Hq=16, Hkv=2, D=128, block=16, sinks=True),
+    dict(P=9001, lens=[33, 700] * 3, n_q=2, Hq=8, Hkv=1, D=64, block=128),
+    dict(P=6000, lens=[600, 4] * 3, n_q=1, Hq=16, Hkv=2, D=256, block=64, sinks=True),
+    # windows that begin in the prefix of some and behind it for others
+    dict(P=3000, lens=[1, 500, 40, 130] * 5, n_q=3, Hq=8, Hkv=2, D=128, block=16, window=400),
+    dict(P=2000, lens=[900, 10] * 10, n_q=1, Hq=16, Hkv=2, D=256, block=32, window=300, sinks=True),
+    dict(P=513, lens=[600] * 20, n_q=2, Hq=8, Hkv=2, D=64, block=16, window=64),
+    # queries inside the prefix (fewer own tokens than queries), and vacant requests
+    dict(P=300, lens=[0, 2, -1, 20, -1, -1] * 4, n_q=6, Hq=8, Hkv=2, D=128, block=16),
+    dict(P=260, lens=[-1] * 70 + [3] * 9, n_q=1, Hq=8, Hkv=1, D=128, block=16, sinks=True),
+    # page sizes from one to two tiles; heads outermost
+    dict(P=777, lens=[100, 7] * 9, n_q=1, Hq=16, Hkv=4, D=128, block=256),
+    dict(P=777, lens=[100, 7] * 9, n_q=1, Hq=16, Hkv=4, D=128, block=128, layout="htd"),
+    dict(P=777, lens=[100, 7] * 9, n_q=1, Hq=16, Hkv=4, D=64, block=32, layout="htd"),
+    # large groups: several row tiles of a request in the paged kernel too
+    dict(P=200, lens=[150, 90, 31], n_q=9, Hq=32, Hkv=1, D=256, block=32),
+    dict(P=200, lens=[150, 90, 31], n_q=5, Hq=128, Hkv=1, D=128, block=16, sinks=True),
+]
+
+
+@pytest.mark.parametrize("kw", MANY, ids=lambda k: "-".join(
+    f"{n}{v if not isinstance(v, list) else len(v)}" for n, v in k.items()))
+def test_many_rows(kw):
+    run_and_compare(make_case(21, **kw), str(kw))
+
+
+def test_many_rows_with_pages_outside_the_cache():
+    c = make_case(22, P=900, lens=[100, 30] * 12, n_q=2, Hq=8, Hkv=2, D=128, block=16)
+    c["pt"][5:9] = c["kc"].shape[0]
+    c["pt"][20:37] = -2 ** 31                        # whole tiles among them
+    c["tables"][3] = -1
+    run_and_compare(c)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_blocks_any_distance_apart(D):
+    # block, token and head strides with no common divisor but 8 elements
+    c = make_case(23, P=300, lens=[70, 20] * 11, n_q=1, Hq=16, Hkv=2, D=D, block=16)
+    nb, bs, H, _ = c["kc"].shape
+    st, sh = H * (D + 8) + 8, D + 8
+    sb = bs * st + 24
+    a = args_dev(c)
+    for n in ("kc", "vc"):
+        t = torch.full((nb * sb,), float("nan"), dtype=torch.bfloat16, device=DEV).as_strided((nb, bs, H, D), (sb, st, sh, 1))
+        t.copy_(c[n])
+        a["k_cache" if n == "kc" else "v_cache"] = t
+    out, lse = swa.thd_attn_shared_prefix(**a)
+    compare(out, lse, reference(c), D)
+
+
+def test_many_rows_captured_follow_lengths():
+    c = make_case(24, P=1500, lens=[300, 200, 100, 50] * 4, n_q=1, Hq=16, Hkv=2, D=128, block=16, window=0)
+    short = dict(c, lens=torch.tensor([17, 200, -1, 0] * 4, dtype=torch.int32), P=129)
+    none = dict(c, pt=None, P=0)
+    a = args_dev(c)
+    n = swa.thd_attn_shared_prefix_workspace_bytes(16, 1, 16, 2, 128)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+    out, lse = torch.zeros((16, 16, 128), dtype=torch.bfloat16, device=DEV), torch.zeros((16, 16), device=DEV)
+    swa.thd_attn_shared_prefix(**a, out=out, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        swa.thd_attn_shared_prefix(**a, out=out, lse=lse, workspace=ws)
+    for case in (short, c, none, short):
+        a["kv_lens"].copy_(case["lens"])
+        a["prefix_len"].fill_(case["P"])
+        g.replay()
+        g.replay()                                          # nothing waits between two steps
+        torch.cuda.synchronize()
+        compare(out, lse, reference(case), 128)
+    assert swa.thd_attn_shared_prefix_get_error() == 0
+
+
+def test_many_rows_on_two_streams_at_once():
+    cases = [make_case(25 + i, P=2500, lens=[900, 30, 500, 64] * 3, n_q=1, Hq=16, Hkv=2, D=128, block=16) for i in range(2)]
+    args = [args_dev(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    res = [[], []]
+    for _ in range(8):
+        for i in (0, 1):
+            res[i].append(swa.thd_attn_shared_prefix(**args[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        compare(*res[i][0], reference(cases[i]), 128)
+        assert all(torch.equal(res[i][0][j], r[j]) for r in res[i] for j in (0, 1))
+
+
+def test_large_scores_and_masked_infinities():
+    # scores of some hundreds, keys behind the window at the type's largest value
+    c = make_case(27, P=600, lens=[40, 9] * 10, n_q=1, Hq=8, Hkv=2, D=128, block=16, window=500, std=6.0)
+    kc, vc = c["kc"], c["vc"]
+    for j in range(0, 90):                                  # (the furthest window begins at 600 + 9 - 500)
+        kc[c["pt"][j // 16], j % 16] = float("inf") if j % 2 else float("-inf")
+        vc[c["pt"][j // 16], j % 16] = 3.3e38 if j % 2 else float("-inf")
+    ref = reference(dict(c, kc=torch.nan_to_num(kc, posinf=0.0, neginf=0.0), vc=torch.nan_to_num(vc, posinf=0.0, neginf=0.0)))
+    out, lse = swa.thd_attn_shared_prefix(**args_dev(c))
+    compare(out, lse, ref, 128)
+
+
+@pytest.mark.parametrize("B", [257, 1025, 8192])
+def test_block_tables_in_place_many(B):
+    rng = np.random.default_rng(B)
+    block, M = 16, 4
+    seq, new = rng.integers(-1, 50, size=B), rng.integers(-1, 20, size=B)
+    held = np.where(seq > 0, -(-seq // block), 0)
+    pool = int(held.sum()) + B // 2
+    perm = rng.permutation(pool).astype(np.int64)
+    table, at = np.full((B, M), -1), 0
+    for b in range(B):
+        table[b, :held[b]] = perm[at:at + held[b]]
+        at += held[b]
+    free = np.full(pool, -1)
+    free[:pool - at] = perm[at:]
+    rows = int(np.where((seq >= 0) & (new > 0), new, 0).sum()) + 3
+    want = OS.block_tables(seq, new, table, free, pool - at, block, rows, 0)
+    d = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32).to(DEV)
+    s, t, f, n = d(seq), d(table), d(free), d([pool - at])
+    r = swa.thd_kv_block_tables(s, d(new), t, f, n, block, rows, seq_lens_out=s, free_count_out=n)
+    got = dict(seq_lens=r[0], cu=r[2], slots=r[3], positions=r[4], table=t, free=f)
+    for name, x in got.items():
+        assert np.array_equal(x.cpu().numpy(), want[name]), name
+    assert n.item() == want["free_count"] and r[5].item() == want["refused"]
+
+
+def test_step_on_another_stream_than_the_current_one():
+    # tables, write and attention on one side stream, nothing on the current one
+    side = torch.cuda.Stream()
+    B, block, M, Hq, Hkv, D = 40, 16, 3, 8, 2, 64
+    d = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32).to(DEV)
+    rng = np.random.default_rng(7)
+    kc, vc = (torch.zeros((B * M, block, Hkv, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    seq, new = d([0] * B), d(rng.integers(1, 30, size=B))
+    table, free, count = d(np.full((B, M), -1)), d(np.arange(B * M)), d([B * M])
+    k, v, q = (workloads.random_bf16(rng, s).to(DEV) for s in ((B * 30, Hkv, D), (B * 30, Hkv, D), (B, Hq, D)))
+    torch.cuda.synchronize()
+    lens, _, cu, slots, _, refused = swa.thd_kv_block_tables(seq, new, table, free, count, block, B * 30, stream=side)
+    swa.thd_kv_write(k, v, slots, kc, vc, stream=side)
+    out, lse = swa.thd_attn_shared_prefix(q, kc, vc, table, lens, stream=side)
+    side.synchronize()
+    assert refused.item() == 0
+    ref = OS.shared_prefix_attention(q.cpu(), kc.cpu(), vc.cpu(), table, lens, None, 0, 0, np.float32(D ** -0.5).item(), None)
+    compare(out, lse, ref, D)
+    host = k.cpu()
+    for b in (0, 17, B - 1):
+        n, first = int(new[b]), int(cu[b])
+        pages = table[b].cpu()
+        for j in (0, n - 1):
+            assert torch.equal(kc[pages[j // block], j % block].cpu(), host[first + j])
