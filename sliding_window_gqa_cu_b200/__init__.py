@@ -673,27 +673,23 @@ def thd_kv_block_tables(seq_lens, new_lens, block_tables, free_blocks, free_coun
     _check_i32("free_count", free_count, (1,), dev)
     if first_position is not None:
         _check_i32("first_position", first_position, (1,), dev)
-    outs = (slots, positions, seq_lens_out, cu_new, free_count_out, refused)
-    sizes = (n_rows, n_rows, B, B + 1, 1, 1)
-    if any(t is not None for t in outs):
-        for name, t, n in zip(("slots", "positions", "seq_lens_out", "cu_new", "free_count_out", "refused"), outs, sizes):
-            if t is not None:
-                _check_i32(name, t, (n,), dev)
-    # What the caller does not pass in comes from one allocation; slots and
-    # positions on 16-byte borders.
-    want = [(i, n) for i, (t, n) in enumerate(zip(outs, sizes)) if t is None]
-    if want:
-        pad = -n_rows % 4
-        parts = [n for i, n in want]
-        at = list(range(len(parts)))
-        if pad and want[0][0] < 2:
-            parts.insert(1, pad)
-            at = [0] + [i + 1 for i in at[1:]]
-        views = _allocate_on(stream, lambda: seq_lens.new_empty((sum(parts),))).split_with_sizes(parts)
-        outs = list(outs)
-        for (i, _), j in zip(want, at):
-            outs[i] = views[j]
-    slots, positions, seq_lens_out, cu_new, free_count_out, refused = outs
+    pad = -n_rows % 4
+    if slots is None and positions is None and seq_lens_out is None and cu_new is None and free_count_out is None \
+            and refused is None:
+        # One allocation for all; slots and positions on 16-byte borders.
+        total = 2 * n_rows + pad + 2 * B + 3
+        buf = seq_lens.new_empty(total) if stream is None else _allocate_on(stream, lambda: seq_lens.new_empty(total))
+        slots, _, positions, seq_lens_out, cu_new, free_count_out, refused = buf.split_with_sizes(
+            (n_rows, pad, n_rows, B, B + 1, 1, 1))
+    else:
+        given = []
+        for name, t, n in (("slots", slots, n_rows), ("positions", positions, n_rows), ("seq_lens_out", seq_lens_out, B),
+                           ("cu_new", cu_new, B + 1), ("free_count_out", free_count_out, 1), ("refused", refused, 1)):
+            if t is None:
+                t = _allocate_on(stream, lambda: seq_lens.new_empty(n))
+            _check_i32(name, t, (n,), dev)
+            given.append(t)
+        slots, positions, seq_lens_out, cu_new, free_count_out, refused = given
     _call_on(dev, stream, lib.thd_kv_block_tables, "thd_kv_block_tables",
              seq_lens.data_ptr(), new_lens.data_ptr(), B, int(block_size), block_tables.data_ptr(), M,
              free_blocks.data_ptr(), free_blocks.shape[0], free_count.data_ptr(),
@@ -780,7 +776,7 @@ def thd_attn_shared_prefix(q, k_cache, v_cache, block_tables, kv_lens, prefix_ta
         if sinks.dtype is not torch.float32 or sinks.device != dev or sinks.numel() != Hq or not sinks.is_contiguous():
             raise ValueError("sinks must be a contiguous fp32 CUDA tensor of Hq values")
     if out is None:
-        out = _allocate_on(stream, lambda: q.new_empty((T, Hq, D)))
+        out = q.new_empty((T, Hq, D)) if stream is None else _allocate_on(stream, lambda: q.new_empty((T, Hq, D)))
     elif out.dtype is not torch.bfloat16 or out.device != dev or out.shape != (T, Hq, D) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bf16 tensor of shape {(T, Hq, D)} on {dev}")
     if lse is None:
