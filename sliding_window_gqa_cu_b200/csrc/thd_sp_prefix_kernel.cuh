@@ -172,9 +172,9 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         *abort_flag = bad;
         fence_barrier_init();
     }
-    if (warp == C::MMA_WARP) {
-        tmem_alloc(smem_addr(tmem_slot), 512);
-        tmem_relinquish();
+    if (threadIdx.x == 32) {
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
     }
     // Least own length (for the first key that any row sees) and all own keys.
     const int P = sp_prefix_len(p);
@@ -195,12 +195,7 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             warp_keys[warp] = keys;
         }
     }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
-    const bool skip = *abort_flag != 0;
-
     PrefixWalk<C> walk;
     {
         int n = 0x7fffffff;
@@ -217,13 +212,23 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         const int my_lane = blockIdx.x / p.pre_width;
         const long long units = sp_prefix_units(p, walk.n_tiles);
         const int lanes = sp_split<C::D>(p, units, keys).lanes;
-        walk.x = my_lane < lanes ? lane_begin(units, lanes, my_lane) : 0;
-        walk.x1 = my_lane < lanes ? lane_begin(units, lanes, my_lane + 1) : 0;
+        walk.x = lanes > 0 ? lane_begin(units, lanes, my_lane) : 0;
+        walk.x1 = lanes > 0 ? lane_begin(units, lanes, my_lane + 1) : 0;
         if (blockIdx.x == 0 && threadIdx.x == 0) {
             p.plan->pre_tiles = walk.n_tiles;
             p.plan->pre_lanes = lanes;
         }
+        if (my_lane >= lanes) return;  // its SM is the paged kernel's
     }
+    if (warp == C::MMA_WARP) {
+        tmem_alloc(smem_addr(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const bool skip = *abort_flag != 0;
     PrefixPiece pc;
 
     if (warp == C::K_WARP || warp == C::V_WARP) {
@@ -231,7 +236,6 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         if (!skip) {
             const bool is_v = warp == C::V_WARP;
             const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
-            if (lane == 0) tma_prefetch_desc(map);
             const int boxes = C::BN / p.box_rows;  // of a slot, one lane each
             const int box = lane < boxes ? lane : 0;
             int pos = 0;        // ring position
