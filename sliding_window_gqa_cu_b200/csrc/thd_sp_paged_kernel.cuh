@@ -9,6 +9,10 @@
 // warp while their 16 KB take longer to arrive.  (A tcgen05 tile would be 128 rows
 // high, 1/16 of it used, and send the scores through TMEM.)
 //
+// P goes into its product as a bf16 number and a second one for what that rounding
+// lost (2^-17 is left): the products are not what bounds the kernel, and a single
+// rounding would add as much error as that of the output.
+//
 // A worker is WR warps of 8 NR rows each, which share a ring of slots (a K or V
 // slice of KS keys each) and refill a slot as soon as it has been read.  Workers
 // never wait for each other.  16 KB a warp, 64 KB a CTA are in flight, three
@@ -59,6 +63,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
+}
+
+// What the packed bf16 pair lost of p0 (low half) and p1, as a bf16 pair.
+__device__ __forceinline__ uint32_t rounding_error(uint32_t packed, float p0, float p1) {
+    return pack_bf16x2(p0 - __uint_as_float(packed << 16), p1 - __uint_as_float(packed & 0xffff0000u));
 }
 
 // c += A B for 16 x 8 x 16, bf16 in, fp32 accumulate.
@@ -455,7 +464,7 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
                 const int key = (pc.slice + j) * C::KS;  // first key of the slice
                 ok = warp_wait(bar(full0 + ks), (pos / C::NSLOT) & 1, abort_flag, status);
                 if (!ok) break;
-                uint32_t pf[C::KS / 16][C::NR][2];
+                uint32_t pf[C::KS / 16][C::NR][2], pl[C::KS / 16][C::NR][2];  // P^T, its rounding errors
                 bool edge = false;
                 if (rows_here) {
                     // 16-key parts whose page exists
@@ -535,8 +544,11 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
                             const float p3 = ex2_approx(fmaf(s[i][t][3], sl2, neg1));
                             l[t][0] += p0 + p2;
                             l[t][1] += p1 + p3;
-                            pf[i][t][0] = transpose8(pack_bf16x2(p0, p1));
-                            pf[i][t][1] = transpose8(pack_bf16x2(p2, p3));
+                            const uint32_t a = pack_bf16x2(p0, p1), b = pack_bf16x2(p2, p3);
+                            pf[i][t][0] = transpose8(a);
+                            pf[i][t][1] = transpose8(b);
+                            pl[i][t][0] = transpose8(rounding_error(a, p0, p1));
+                            pl[i][t][1] = transpose8(rounding_error(b, p2, p3));
                         }
                     }
                 }
@@ -573,7 +585,10 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
                                     a[3] &= keep1;
                                 }
 #pragma unroll
-                                for (int t = 0; t < C::NR; ++t) mma16816(acc[d][t], a, pf[i][t][0], pf[i][t][1]);
+                                for (int t = 0; t < C::NR; ++t) {
+                                    mma16816(acc[d][t], a, pf[i][t][0], pf[i][t][1]);
+                                    mma16816(acc[d][t], a, pl[i][t][0], pl[i][t][1]);
+                                }
                             }
                         }
                     };

@@ -630,7 +630,9 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                     const float2 sl2x2 = make_float2(sl2, sl2);
                     const float2 negm2 = make_float2(neg_m, neg_m);
                     float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-                    // P of CK keys over the first half of their score columns: the second chunk
+                    // P (rounded to bf16 once: another product for what that loses, as in the
+                    // paged kernel, would add half of the products, which bound this one)
+                    // of CK keys over the first half of their score columns: the second chunk
                     // is still in registers, the first is read again (holding both would
                     // spill).
                     auto publish = [&](int i) {
