@@ -557,7 +557,8 @@ int thd_attn_shared_prefix(const void* q, const void* k_cache, const void* v_cac
                            const float* sinks_or_null, void* out, float* lse,
                            void* workspace, size_t workspace_bytes, void* stream);
 /* Synchronises the stream; returns and clears the status word of
- * thd_attn_shared_prefix on the current device. */
+ * thd_attn_shared_prefix on the current device.  While it is not 0 calls write
+ * nothing. */
 int thd_attn_shared_prefix_get_error(void* stream);
 
 /* ABI version of this header: (major << 16) | minor. */

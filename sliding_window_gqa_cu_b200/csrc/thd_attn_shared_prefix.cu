@@ -43,7 +43,7 @@ __device__ int g_sp_status;
 // (Nothing branches on a part's maximum: the compiler would move the loads behind
 // the branch, one latency after the other.)
 template <int D>
-__global__ void __launch_bounds__(512) thd_sp_merge_kernel(const SpParams p) {
+__global__ void __launch_bounds__(512) thd_sp_merge_kernel(const SpParams p, const int* status) {
     constexpr int NT = thd::PrefixConfig<D>::NT;
     constexpr int BATCH = 4;
     constexpr int WARPS = D < 128 ? D / 16 : 8;  // of a run
@@ -63,6 +63,8 @@ __global__ void __launch_bounds__(512) thd_sp_merge_kernel(const SpParams p) {
     const int h = blockIdx.x / groups, row0 = (blockIdx.x - h * groups) * 8;
     const bool quads = p.pre_lanes > 0;  // the prefix's parts are the prefix kernel's
     thd::wait_for_previous_grid();
+    // After a stall the places of the parts may not have been written: leave the rows.
+    if (*reinterpret_cast<const volatile int*>(status) != 0) return;
     if (threadIdx.x < 16) {
         const int which = threadIdx.x >> 3, r = min(row0 + static_cast<int>(threadIdx.x & 7), p.rows - 1);
         const int b = r / p.RB, rr = r - b * p.RB;
@@ -363,7 +365,8 @@ int launch_all(SpParams p, const Maps& maps, cudaStream_t stream) {
     }
     const int64_t ctas = static_cast<int64_t>(p.Hkv) * ((p.rows + 7) / 8);
     if (!launch_early(thd_sp_merge_kernel<D>, dim3(static_cast<unsigned>(ctas), D > 128 ? D / 128 : 1),
-                      D < 128 ? 4 * D : 512, 0, stream, early, p))
+                      D < 128 ? 4 * D : 512, 0, stream, early,
+                      static_cast<const SpParams&>(p), static_cast<const int*>(st)))
         return THD_ERR_CUDA;
     return THD_OK;
 }

@@ -17,10 +17,10 @@
 // lengths (sp_split): the CTAs beyond leave their SMs to the paged kernel.
 //
 // Warps: 8 softmax warps (a thread a row; D = 256: two), a TMA producer for K and
-// one for V, an MMA issuer for each row tile.  A TMA box holds a page's tokens (128 at most) x all
-// columns of a slot: [tokens / 8][column chunk][8 tokens][64 columns], whose
-// groups of 8 tokens have one stride over the pages of a tile, as the matrix
-// descriptors need it.
+// one for V, an MMA issuer for each row tile.  A TMA box holds a page's tokens
+// (128 at most) x all columns of a slot: [tokens / 8][column chunk][8 tokens][64
+// columns], whose groups of 8 tokens have one stride over the pages of a tile, as
+// the matrix descriptors need it.
 #pragma once
 
 #include "thd_attn_kernel.cuh"
@@ -323,8 +323,8 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                 if (!elect_one()) return;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ts(d_tmem, p_tmem + kk * 16 / C::CK * C::CK + kk * 16 % C::CK / 2, dv + ((kk * 2 * C::GROUP_BYTES) >> 4), idesc_pv,
-                                acc || kk > 0 ? 1u : 0u);
+                    mma_bf16_ts(d_tmem, p_tmem + kk * 16 / C::CK * C::CK + kk * 16 % C::CK / 2,
+                                dv + ((kk * 2 * C::GROUP_BYTES) >> 4), idesc_pv, acc || kk > 0 ? 1u : 0u);
             };
             auto commit = [&](int idx) {
                 if (elect_one()) mma_commit(bar(idx));
