@@ -114,7 +114,7 @@ def block_tables(seq_lens, new_lens, table, free_blocks, free_count, block, n_ro
             wanted += need
         refused += no
         seq_out.append(n if no else n + m)
-        for x in range(n, n + m):
+        for x in range(n, n + min(m, n_rows - len(slots))):     # (rows behind the call's are not given)
             slots.append(-1 if no else int(table[b, x // block]) * block + x % block)
             positions.append(first_position + x)
     pad = max(0, n_rows - len(slots))
