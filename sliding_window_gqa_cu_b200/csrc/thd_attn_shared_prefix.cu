@@ -10,8 +10,8 @@
 //   thd_sp_paged_kernel   each request's own pages (bound by memory); it runs
 //                         on the SMs that the prefix kernel leaves
 //   thd_sp_merge_kernel   adds the parts and the sinks, divides, writes
-// With few rows in all (one row tile of the paged kernel) that kernel takes the
-// prefix as well and the first launch falls away.
+// With few rows on a short prefix the paged kernel takes that as well and the first
+// launch falls away.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -210,9 +210,22 @@ __global__ void __launch_bounds__(512) thd_sp_merge_kernel(const SpParams p, con
 
 constexpr int kMaxUnits = 4096;
 constexpr int kPagedCtas = 3 * thd::kSpLanes;  // three fit an SM
-// The paged kernel takes the prefix too when all rows of a kv head fit one row
-// tile of this many.
-constexpr int kPagedPrefixRows = 32;
+// Up to this many rows of a kv head the blocks may lie any distance apart (the paged
+// kernel takes the prefix where the prefix kernel's map cannot).
+constexpr int kAnyPlacesRows = 32;
+
+// Whether the paged kernel takes a prefix (of at most `tokens`, what its table
+// holds) too, once per row tile: it is done with few keys before another launch
+// has started.  Same rows and heads (8 of 128), paged against prefix kernel, us:
+// 16 rows 8,191 keys 32 and 36, 65,536 keys 116 and 84; 32 rows 37 and 38, 173 and
+// 103; 64 rows 1,000 keys 22 and 27, 8,191 keys 44 and 38.  Tiles of more rows are
+// bound by products and those of 256 columns have slower slices: 16 rows of a
+// request, 4,000 keys 34 and 32.  One tile of 8 rows leaves the prefix kernel
+// nothing to share (65,536 keys 75 and 84).
+bool prefix_by_pages(int tiles, int tile_rows, int64_t tokens, int D) {
+    if (tile_rows == 8 && D <= 128) return tiles == 1 || tokens * tiles * tile_rows <= 1 << 18;
+    return tokens <= 2048 && tokens * tiles * tile_rows <= 1 << 18;
+}
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -231,9 +244,7 @@ Layout make_layout(int n_req, int n_q, int Hq, int Hkv, int D) {
     Layout y{};
     y.RB = n_q * (Hq / Hkv);
     y.rows = n_req * y.RB;
-    const bool small = y.rows <= kPagedPrefixRows;
-    const int want = small ? y.rows : y.RB;
-    y.pg_rows = want <= 8 ? 8 : want <= 16 ? 16 : want <= 32 || D == 256 ? 32 : 64;
+    y.pg_rows = y.RB <= 8 ? 8 : y.RB <= 16 ? 16 : y.RB <= 32 || D == 256 ? 32 : 64;
     y.pg_units = (y.RB + y.pg_rows - 1) / y.pg_rows;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -250,34 +261,37 @@ Layout make_layout(int n_req, int n_q, int Hq, int Hkv, int D) {
     const int warp_rows = y.pg_rows == 8 || D == 256 ? 8 : 16;
     y.pg_cont = take(static_cast<size_t>(kPagedCtas) * 4 * warp_rows * D * 4);
     y.pg_cont_ml = take(static_cast<size_t>(kPagedCtas) * 4 * warp_rows * 8);
-    if (small) {
-        y.pg_prefix = 1;
-        y.pgp_home = take(static_cast<size_t>(Hkv) * y.pg_rows * D * 4);
-        y.pgp_home_ml = take(static_cast<size_t>(Hkv) * y.pg_rows * 8);
-        y.pgp_desc = take(static_cast<size_t>(Hkv) * 8);
-    } else {
-        const int tile = D == 256 ? 128 : 256;  // rows of a group
-        y.pre_groups = (y.rows + tile - 1) / tile;
-        // Groups in step: as many as keep the CTAs busy (idle ones and empty
-        // places of the last bundle cost their share, reading K and V for fewer
-        // groups at once about 0.15 / width).
-        double best = -1.0;
-        for (int w = 1; w <= std::min(y.pre_groups, 8); ++w) {
-            const int bundles = (y.pre_groups + w - 1) / w, lanes = thd::kSpLanes / w;
-            const double busy = static_cast<double>(y.pre_groups) / (bundles * w) * (lanes * w) / thd::kSpLanes;
-            const double score = busy / (1.0 + 0.15 / w);
-            if (score > best) {
-                best = score;
-                y.pre_width = w;
-                y.pre_lanes = lanes;
-            }
+    // The prefix's parts, of the paged kernel or in the same place of the prefix kernel.
+    const size_t shared = at;
+    y.pg_prefix = (y.rows + y.pg_rows - 1) / y.pg_rows;
+    const size_t tiles = static_cast<size_t>(y.pg_prefix) * Hkv;
+    y.pgp_home = take(tiles * y.pg_rows * D * 4);
+    y.pgp_home_ml = take(tiles * y.pg_rows * 8);
+    y.pgp_desc = take(tiles * 8);
+    const size_t end = at;
+    at = shared;
+    const int tile = D == 256 ? 128 : 256;  // rows of a group
+    y.pre_groups = (y.rows + tile - 1) / tile;
+    // Groups in step: as many as keep the CTAs busy (idle ones and empty
+    // places of the last bundle cost their share, reading K and V for fewer
+    // groups at once about 0.15 / width).
+    double best = -1.0;
+    for (int w = 1; w <= std::min(y.pre_groups, 8); ++w) {
+        const int bundles = (y.pre_groups + w - 1) / w, lanes = thd::kSpLanes / w;
+        const double busy = static_cast<double>(y.pre_groups) / (bundles * w) * (lanes * w) / thd::kSpLanes;
+        const double score = busy / (1.0 + 0.15 / w);
+        if (score > best) {
+            best = score;
+            y.pre_width = w;
+            y.pre_lanes = lanes;
         }
-        const size_t padded = static_cast<size_t>(y.pre_groups) * tile;
-        y.pre_home = take(padded * Hkv * D * 4);
-        y.pre_home_ml = take(padded * Hkv * 8);
-        y.pre_cont = take(static_cast<size_t>(thd::kSpLanes) * tile * D * 4);
-        y.pre_cont_ml = take(static_cast<size_t>(thd::kSpLanes) * tile * 8);
     }
+    const size_t padded = static_cast<size_t>(y.pre_groups) * tile;
+    y.pre_home = take(padded * Hkv * D * 4);
+    y.pre_home_ml = take(padded * Hkv * 8);
+    y.pre_cont = take(static_cast<size_t>(thd::kSpLanes) * tile * D * 4);
+    y.pre_cont_ml = take(static_cast<size_t>(thd::kSpLanes) * tile * 8);
+    at = std::max(at, end);
     y.bytes = at;
     return y;
 }
@@ -426,6 +440,12 @@ extern "C" int thd_attn_shared_prefix(const void* q, const void* k_cache, const 
     if (!any_keys) prefix_blocks = max_blocks = 0;
     const bool prefix = prefix_blocks > 0;
     const Layout y = make_layout(n_req, n_q, Hq, Hkv, D);
+    // The prefix kernel's map counts places in units of the strides' divisor.
+    const int64_t bs = num_blocks > 1 ? block_stride : 0, hs = Hkv > 1 ? head_stride : 0;
+    const int64_t g = std::max<int64_t>(std::gcd(bs, hs), 8);
+    const int64_t places = any_keys ? (num_blocks - 1) * (bs / g) + (Hkv - 1) * (hs / g) + 1 : 0;
+    if (prefix && places > kMax && y.rows > kAnyPlacesRows) return THD_ERR_UNSUPPORTED;
+    const bool by_pages = places > kMax || prefix_by_pages(y.pg_prefix, y.pg_rows, static_cast<int64_t>(prefix_blocks) * block_size, D);
     char* ws = static_cast<char*>(workspace);
     auto f = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
     auto f2 = [&](size_t at) { return reinterpret_cast<float2*>(ws + at); };
@@ -462,7 +482,7 @@ extern "C" int thd_attn_shared_prefix(const void* q, const void* k_cache, const 
     p.box_rows = std::min(block_size, 128);
     p.pre_groups = y.pre_groups;
     p.pre_width = y.pre_width;
-    p.pre_lanes = prefix ? y.pre_lanes : 0;
+    p.pre_lanes = prefix && !by_pages ? y.pre_lanes : 0;
     p.pre_home = f(y.pre_home);
     p.pre_home_ml = f2(y.pre_home_ml);
     p.pre_cont = f(y.pre_cont);
@@ -470,7 +490,7 @@ extern "C" int thd_attn_shared_prefix(const void* q, const void* k_cache, const 
     p.plan = reinterpret_cast<thd::SpPlan*>(ws + y.plan);
     p.pg_rows = y.pg_rows;
     p.pg_units = y.pg_units;
-    p.pg_prefix = prefix ? y.pg_prefix : 0;
+    p.pg_prefix = prefix && by_pages ? y.pg_prefix : 0;
     p.own_home = f(y.own_home);
     p.own_home_ml = f2(y.own_home_ml);
     p.own_desc = i8(y.own_desc);
@@ -481,10 +501,6 @@ extern "C" int thd_attn_shared_prefix(const void* q, const void* k_cache, const 
     p.pg_cont_ml = f2(y.pg_cont_ml);
     Maps maps{};
     if (any_keys && p.pre_lanes > 0) {
-        const int64_t bs = num_blocks > 1 ? block_stride : 0, hs = Hkv > 1 ? head_stride : 0;
-        const int64_t g = std::max<int64_t>(std::gcd(bs, hs), 8);
-        const int64_t places = (num_blocks - 1) * (bs / g) + (Hkv - 1) * (hs / g) + 1;
-        if (places > kMax) return THD_ERR_UNSUPPORTED;
         p.places = static_cast<int>(places);
         p.place_block = static_cast<int>(bs / g);
         p.place_head = static_cast<int>(hs / g);

@@ -156,22 +156,28 @@ struct SpSplit {
 // products and softmax, the paged kernel by memory, which half of the SMs can
 // keep busy, so both run side by side and the choice that ends the later one
 // soonest is taken.  The prefix takes kStart + tile * units / lanes; the requests'
-// own keys kStartPaged + bytes at kSmRate per SM, kMemRate at most (ns, and bytes
-// a ns, as measured).  Every thread has its own candidates; the best of the warp
-// wins.  64 requests on 8,191 tokens 92 us one after the other, 78 side by side,
-// 256 on 32,768 474 and 393; both kernels' CTAs on the same SM 96 and 638 (the
-// softmax warps lose more by waiting for issue slots and loads than memory gains).
+// own keys kStartPaged + bytes at an SM's rate each, kMemRate at most (ns, and bytes
+// a ns, as measured; row tiles of 32 and more are bound by their products, about
+// 0.57 TFLOP/s an SM, and read an item's keys once each).  Every thread has its own
+// candidates; the best of the warp wins.  64 requests on 8,191 tokens 92 us one
+// after the other, 75 side by side, 256 on 32,768 474 and 400; both kernels' CTAs on
+// the same SM 96 and 638 (the softmax warps lose more by waiting for issue slots and
+// loads than memory gains).  One rate for all row tiles: 64 requests of 16 rows,
+// 32,000 + 50..200 tokens, 272 against 165; one of 64 rows, 65,536 + 2,048, 446
+// against 96.
 template <int D>
 __device__ __forceinline__ SpSplit sp_split(const SpParams& p, long long units, float own_keys) {
-    constexpr float kMemRate = 5000.0f, kSmRate = 80.0f, kStart = 10000.0f, kStartPaged = 12000.0f;
+    constexpr float kMemRate = 6000.0f, kStart = 10000.0f, kStartPaged = 12000.0f;
+    constexpr float kSmRate = D == 64 ? 60.0f : 76.0f, kSmRate16 = D == 64 ? 55.0f : 50.0f, kSmRows = 570.0f;
     constexpr float kTile = D == 64 ? 1600.0f : 2300.0f;
-    const float bytes = own_keys * p.Hkv * (D * 4);
+    const float bytes = own_keys * p.Hkv * p.pg_units * (D * 4);
+    const float sm_rate = p.pg_rows <= 8 ? kSmRate : p.pg_rows <= 16 ? kSmRate16 : kSmRows / p.pg_rows;
     const int most = units > 0 ? sp_prefix_lanes(p, units) : 0;
     float best = INFINITY;
     int lanes = most;
     for (int l = 1 + static_cast<int>(threadIdx.x & 31); l <= most; l += 32) {
         const float prefix = kStart + kTile * (static_cast<float>(units) / l);
-        const float rate = fminf(kMemRate, (kSpLanes - l * p.pre_width) * kSmRate);
+        const float rate = fminf(kMemRate, (kSpLanes - l * p.pre_width) * sm_rate);
         const float time = bytes > 0.0f ? fmaxf(prefix, kStartPaged + bytes / rate) : prefix;
         if (time <= best) {
             best = time;

@@ -669,3 +669,69 @@ def test_step_on_another_stream_than_the_current_one():
         pages = table[b].cpu()
         for j in (0, n - 1):
             assert torch.equal(kc[pages[j // block], j % block].cpu(), host[first + j])
+
+
+# The same with a prefix table that could hold a long prefix: which kernel takes
+# the prefix goes by what the table holds (above 8 rows the prefix kernel takes
+# 32,768 keys, and below them the paged kernel).
+
+WIDE = [kw for kw in CASES + MANY if kw["P"] > 0]
+
+
+@pytest.mark.parametrize("kw", WIDE, ids=lambda k: "-".join(
+    f"{n}{v if not isinstance(v, list) else len(v)}" for n, v in k.items()))
+def test_wide_prefix_tables(kw):
+    c = make_case(31, **kw)
+    wide = torch.full((32768 // kw["block"],), -1, dtype=torch.int32)
+    wide[:len(c["pt"])] = c["pt"]
+    a = args_dev(dict(c, pt=wide))
+    out, lse = swa.thd_attn_shared_prefix(**a)
+    assert swa.thd_attn_shared_prefix_get_error() == 0
+    compare(out, lse, reference(c), kw["D"], str(kw))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,lens,n_q", [(128, 8, 2, [40, 3], 1), (64, 4, 4, [200], 5), (128, 8, 1, [700, 1, -1, 90], 1),
+                                               (256, 8, 1, [20] * 3, 1), (128, 8, 2, [0, 33] * 8, 4)])
+def test_wide_prefix_tables_captured_follow_the_prefix(D, Hq, Hkv, lens, n_q):
+    c = make_case(32, P=32768, lens=lens, n_q=n_q, Hq=Hq, Hkv=Hkv, D=D, block=64, sinks=True)
+    a = args_dev(c)
+    T = len(lens) * n_q
+    out, lse = torch.zeros((T, Hq, D), dtype=torch.bfloat16, device=DEV), torch.zeros((T, Hq), device=DEV)
+    swa.thd_attn_shared_prefix(**a, out=out, lse=lse)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        swa.thd_attn_shared_prefix(**a, out=out, lse=lse)
+    for P in (2500, 0, 65, 2500):
+        a["prefix_len"].fill_(P)
+        g.replay()
+        torch.cuda.synchronize()
+        # (slots of the table's pages behind P are not seen)
+        compare(out, lse, reference(dict(c, P=P)), D, f"P={P}")
+    assert swa.thd_attn_shared_prefix_get_error() == 0
+
+
+def test_blocks_far_apart_with_few_rows():
+    # 2^31 places for the prefix kernel's map (strides share 8 elements): with few rows
+    # the paged kernel takes a long table too
+    D, Hq, Hkv, block, nb = 64, 8, 2, 16, (1 << 20) + 1
+    sb, st, sh = (1 << 14) + 16, Hkv * (D + 8), D + 8
+    c = make_case(33, P=700, lens=[40, 9], n_q=2, Hq=Hq, Hkv=Hkv, D=D, block=block)
+    n = c["kc"].shape[0]
+    far = lambda t: torch.where((t >= 0) & (t < n), t * ((nb - 1) // (n - 1)), -1).int()
+    a = args_dev(c)
+    wide = torch.full((32768 // block,), -1, dtype=torch.int32)
+    wide[:len(c["pt"])] = far(c["pt"])
+    a["prefix_table"], a["block_tables"] = wide.to(DEV), far(c["tables"]).to(DEV)
+    both = torch.empty((nb * sb,), dtype=torch.bfloat16, device=DEV)     # 34 GB, most of it not touched
+    at = far(torch.arange(n)).long().to(DEV)
+    for i, name in enumerate(("k", "v")):
+        cache = both.as_strided((nb, block, Hkv, D), (sb, st, sh, 1), i * 8192)
+        cache[at] = c[name + "c"].to(DEV)
+        a[name + "_cache"] = cache
+    out, lse = swa.thd_attn_shared_prefix(**a)
+    compare(out, lse, reference(c), D)
+    many = torch.zeros((9 * 2, Hq, D), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(swa.ThdAttnError):                                # 72 rows a kv head
+        swa.thd_attn_shared_prefix(**dict(a, q=many, block_tables=a["block_tables"][:1].expand(9, -1).contiguous(),
+                                          kv_lens=a["kv_lens"][:1].expand(9).contiguous()))
