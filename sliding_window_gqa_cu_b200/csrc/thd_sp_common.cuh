@@ -25,6 +25,8 @@
 
 #include <cstdint>
 
+#include "sp_lanes.h"
+
 namespace thd {
 
 constexpr int kSpLanes = 148;  // CTAs of the prefix kernel (one per SM)
@@ -89,22 +91,6 @@ struct SpParams {
 // 16 bytes into shared memory, zeros if !there.
 __device__ __forceinline__ void load16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-
-// (32-bit division where it is enough: the 64-bit one takes some 100 instructions.)
-// First unit of lane l when `units` are cut into `lanes` ranges (lanes <= units,
-// so that none is empty).
-__device__ __forceinline__ long long lane_begin(long long units, int lanes, int l) {
-    const unsigned long long at = static_cast<unsigned long long>(units) * l;
-    if (at >> 32 == 0) return static_cast<unsigned>(at) / static_cast<unsigned>(lanes);
-    return static_cast<long long>(at / static_cast<unsigned>(lanes));
-}
-
-// The lane that holds unit x: the largest l with units * l / lanes < x + 1.
-__device__ __forceinline__ int lane_of(long long units, int lanes, long long x) {
-    const unsigned long long at = static_cast<unsigned long long>(x + 1) * lanes - 1;
-    if (at >> 32 == 0) return static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(units));
-    return static_cast<int>(at / static_cast<unsigned long long>(units));
 }
 
 // Lanes that the prefix kernel's units are cut over at most: three units each (a part costs
