@@ -470,8 +470,10 @@ int thd_sparse_mla_get_error(void* stream);
  *   refused             int32 [1]: how many requests were refused
  * 1 <= n_req <= 8192 (else THD_ERR_UNSUPPORTED), n_rows >= 0, block_size >= 1,
  * max_blocks >= 1, free_capacity >= 0; all pointers 4-byte aligned.
- * n_req = 0 is a no-op.  Deterministic (no atomics).  One launch.  Apart from
- * the arrays that may be the same, outputs must not overlap inputs.
+ * n_req = 0 is a no-op that leaves every output as it is: the caller keeps its
+ * free_count (the Python binding writes the outputs then).  Deterministic (no
+ * atomics).  One launch.  Apart from the arrays that may be the same, outputs
+ * must not overlap inputs.
  */
 int thd_kv_block_tables(const int32_t* seq_lens, const int32_t* new_lens, int n_req, int block_size,
                         int32_t* block_tables, int max_blocks,

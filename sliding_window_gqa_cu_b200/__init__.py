@@ -657,7 +657,8 @@ def thd_kv_block_tables(seq_lens, new_lens, block_tables, free_blocks, free_coun
     positions (a shared prefix's length) or None.  Returns ``(seq_lens_out,
     free_count_out, cu_new [B + 1], slots [n_rows], positions [n_rows],
     refused [1])``; each may be passed in (``seq_lens_out`` may be ``seq_lens``
-    and ``free_count_out`` may be ``free_count``).
+    and ``free_count_out`` may be ``free_count``).  Without requests the count is
+    handed on and every row has slot -1.
     """
     lib = load_library()
     _check_cuda("seq_lens", seq_lens)
@@ -696,6 +697,15 @@ def thd_kv_block_tables(seq_lens, new_lens, block_tables, free_blocks, free_coun
              first_position.data_ptr() if first_position is not None else None, n_rows,
              seq_lens_out.data_ptr(), free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
              positions.data_ptr(), refused.data_ptr())
+    if B == 0:
+        import torch
+
+        # The library writes nothing then: an idle step keeps its pool and has no slots.
+        with torch.cuda.stream(stream):
+            free_count_out.copy_(free_count.clamp(0, free_blocks.shape[0]))
+            slots.fill_(-1)
+            for t in (positions, cu_new, refused):
+                t.zero_()
     return seq_lens_out, free_count_out, cu_new, slots, positions, refused
 
 
