@@ -473,7 +473,9 @@ int thd_sparse_mla_get_error(void* stream);
  * n_req = 0 is a no-op that leaves every output as it is: the caller keeps its
  * free_count (the Python binding writes the outputs then).  Deterministic (no
  * atomics).  One launch.  Apart from the arrays that may be the same, outputs
- * must not overlap inputs.
+ * must not overlap inputs.  A graph that is replayed step after step needs
+ * seq_lens_out = seq_lens and free_count_out = free_count (block_tables and
+ * free_blocks always are in place): otherwise every replay takes the same step.
  */
 int thd_kv_block_tables(const int32_t* seq_lens, const int32_t* new_lens, int n_req, int block_size,
                         int32_t* block_tables, int max_blocks,

@@ -657,8 +657,9 @@ def thd_kv_block_tables(seq_lens, new_lens, block_tables, free_blocks, free_coun
     positions (a shared prefix's length) or None.  Returns ``(seq_lens_out,
     free_count_out, cu_new [B + 1], slots [n_rows], positions [n_rows],
     refused [1])``; each may be passed in (``seq_lens_out`` may be ``seq_lens``
-    and ``free_count_out`` may be ``free_count``).  Without requests the count is
-    handed on and every row has slot -1.
+    and ``free_count_out`` may be ``free_count``: a captured step that is replayed
+    needs both in place, or every replay begins from the same lengths and free
+    pages).  Without requests the count is handed on and every row has slot -1.
     """
     lib = load_library()
     _check_cuda("seq_lens", seq_lens)

@@ -1,12 +1,18 @@
 """The serving step as a server runs it: steps without requests, steps replayed
 from a captured graph, block tables of every size class."""
+import os
+import re
+import textwrap
+
 import numpy as np
 import pytest
 import torch
 
+from oracle import prologue as OP
 from oracle import serving as OS
 import sliding_window_gqa_cu_b200 as swa
-from sliding_window_gqa_cu_b200 import build
+from sliding_window_gqa_cu_b200 import build, workloads
+from test_serving_gpu import compare
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -84,3 +90,116 @@ def test_idle_step_then_tokens():
     lens, count, _, slots, _, refused = swa.thd_kv_block_tables(i32([0]), i32([5]), table, free, count, 4, 6)
     assert refused.item() == 0 and count.item() == 2 and lens.tolist() == [5] and table.tolist() == [[8, 7]]
     assert slots.tolist() == [32, 33, 34, 35, 28, -1]
+
+
+# -------------------------------------------------- a captured step, replayed
+
+README = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+
+
+def documented_step():
+    """The code of the step that users are shown."""
+    text = open(README).read()
+    block = re.search(r"## A serving step\n(.*?)\n## ", text, flags=re.S).group(1)
+    return textwrap.dedent("\n".join(line for line in block.split("\n") if line.startswith("    ")))
+
+
+@pytest.mark.parametrize("window,with_sinks", [(0, False), (50, True)])
+def test_the_documented_step_replays_from_a_graph(window, with_sinks):
+    """The documented step is captured once; every replay takes the step after the
+    one before: new pages, slots and positions, nothing of the step before written
+    over, and the attention over all tokens so far, against the oracle's own state."""
+    B, block, M, Hq, Hkv, D, P = 6, 16, 6, 8, 2, 64, 37
+    rng = np.random.default_rng(3)
+    n_rows, pool, pages = B + 2, 40, -(-P // block)
+    perm = rng.permutation(pool).astype(np.int64)
+    # the oracle's state; requests of 0, 15, 16, 31 and 33 tokens and a vacant entry
+    seq, table = np.array([0, 15, 16, -1, 31, 33]), np.full((B, M), -1, dtype=np.int64)
+    at = pages
+    for b in range(B):
+        held = -(-max(seq[b], 0) // block)
+        table[b, :held] = perm[at:at + held]
+        at += held
+    free, count = np.full(pool, -1, dtype=np.int64), pool - at
+    free[:count] = perm[at:]
+    cache = [workloads.random_bf16(rng, (pool, block, Hkv, D)) for _ in range(2)]
+    sinks = torch.from_numpy(rng.standard_normal(Hq).astype(np.float32)) if with_sinks else None
+    rows = lambda h: workloads.random_bf16(rng, (n_rows, h, D))
+
+    q, k, v = (torch.zeros((n_rows, h, D), dtype=torch.bfloat16, device=DEV) for h in (Hq, Hkv, Hkv))
+    ns = dict(lens=i32(seq), new_lens=i32([1] * B), block_tables=i32(table), free_blocks=i32(free), n_free=i32([count]),
+              block_size=block, n_rows=n_rows, prefix_len=i32([P]), q=q, k=k, v=v, k_cache=cache[0].to(DEV),
+              v_cache=cache[1].to(DEV), q_last=torch.zeros((B, Hq, D), dtype=torch.bfloat16, device=DEV),
+              prefix_table=i32(perm[:pages]), window=window, sinks=sinks.to(DEV) if with_sinks else None,
+              workspace=torch.empty((swa.thd_attn_shared_prefix_workspace_bytes(B, 1, Hq, Hkv, D),), dtype=torch.uint8,
+                                    device=DEV))
+    state = {n: ns[n] for n in ("lens", "n_free", "block_tables", "free_blocks", "k_cache", "v_cache")}
+    before = {n: t.clone() for n, t in state.items()}
+    code = compile(documented_step(), "documented step", "exec")
+    exec(code, dict(ns))                                   # (a first, eager call; its state is put back)
+    for n, t in state.items():
+        t.copy_(before[n])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        exec(code, ns)
+    for step in range(36):
+        new = np.ones(B, dtype=np.int64)
+        if step == 5:
+            new[1] = -1                                    # a request ends,
+        if step == 9:
+            seq[1] = 0                                     # and another takes its entry
+            state["lens"][1] = 0
+        if step == 20:
+            new[2] = 0                                     # a request pauses
+        qh, kh, vh = rows(Hq), rows(Hkv), rows(Hkv)
+        for t, x in ((q, qh), (k, kh), (v, vh)):
+            t.copy_(x)
+        ns["q_last"].copy_(qh[:B])
+        ns["new_lens"].copy_(torch.from_numpy(new))
+        g.replay()
+        torch.cuda.synchronize()
+        want = OS.block_tables(seq, new, table, free, count, block, n_rows, P)
+        check_outputs((state["lens"], state["n_free"], ns["cu"], ns["slots"], ns["positions"], ns["refused"]), want)
+        seq, count, table, free = want["seq_lens"], want["free_count"], want["table"], want["free"]
+        assert want["refused"] == 0
+        assert np.array_equal(state["block_tables"].cpu().numpy(), table) and \
+            np.array_equal(state["free_blocks"].cpu().numpy(), free)
+        # the rotated rows (rounded to bf16 once; angles below 2^7 in fp32 are off by at
+        # most 2^-17, values are at most sqrt(D) = 8), and every row where it belongs
+        kd, kr = k.cpu(), OP.qk_norm_rope(kh, None, positions=want["positions"])
+        assert (np.abs(kd.double().numpy() - kr) <= 2.0 ** -8 * np.abs(kr) + 2.0 ** -13).all()
+        for i, (x, dev) in enumerate(((kd, state["k_cache"]), (vh, state["v_cache"]))):
+            for r, slot in enumerate(want["slots"]):
+                if slot >= 0:
+                    cache[i][slot // block, slot % block] = x[r]
+            assert torch.equal(dev.cpu(), cache[i])
+        ref = OS.shared_prefix_attention(ns["q_last"].cpu(), *cache, table, seq, perm[:pages], P, window,
+                                         np.float32(D ** -0.5).item(), sinks)
+        compare(ns["out"], ns["lse"], ref, D, f"step {step}")
+    assert swa.thd_attn_shared_prefix_get_error() == 0
+
+
+@pytest.mark.parametrize("B", [40, 300, 3001])
+def test_tables_in_place_replay_from_a_graph(B):
+    # one CTA, a cluster of CTAs
+    rng = np.random.default_rng(B)
+    block, M, n_rows = 4, 8, B + 5
+    pool = B * M
+    seq, table = np.zeros(B, dtype=np.int64), np.full((B, M), -1, dtype=np.int64)
+    free, count = rng.permutation(pool).astype(np.int64), pool
+    lens, new_d, tab, fr, n = i32(seq), i32(np.ones(B)), i32(table), i32(free), i32([count])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = swa.thd_kv_block_tables(lens, new_d, tab, fr, n, block, n_rows, seq_lens_out=lens, free_count_out=n)
+    for step in range(12):
+        new = rng.integers(0, 2, size=B)
+        new[rng.uniform(size=B) < 0.05] = -1
+        new_d.copy_(torch.from_numpy(new))
+        seq = np.where((seq < 0) & (rng.uniform(size=B) < 0.5), 0, seq)     # entries are taken again
+        lens.copy_(torch.from_numpy(seq))
+        g.replay()
+        want = OS.block_tables(seq, new, table, free, count, block, n_rows)
+        check_outputs(got, want)
+        seq, count, table, free = want["seq_lens"], want["free_count"], want["table"], want["free"]
+        assert np.array_equal(tab.cpu().numpy(), table) and np.array_equal(fr.cpu().numpy(), free)
