@@ -560,9 +560,13 @@ int thd_attn_shared_prefix(const void* q, const void* k_cache, const void* v_cac
                            int n_req, int n_q, int Hq, int Hkv, int D, int window, float scale,
                            const float* sinks_or_null, void* out, float* lse,
                            void* workspace, size_t workspace_bytes, void* stream);
-/* Synchronises the stream; returns and clears the status word of
- * thd_attn_shared_prefix on the current device.  While it is not 0 calls write
- * nothing. */
+/* Synchronises the stream and returns the status of the last stall of
+ * thd_attn_shared_prefix on the current device that this stream has not been
+ * told of yet, THD_OK if there is none.  After a stall the calls of all streams
+ * write nothing until one of them asks here; that one waits for the whole device,
+ * and the others hear of it when they ask (as does, once, a stream that asks for
+ * the first time).  Not THD_OK: what this stream's calls since it last asked
+ * should have written may not be there. */
 int thd_attn_shared_prefix_get_error(void* stream);
 
 /* ABI version of this header: (major << 16) | minor. */

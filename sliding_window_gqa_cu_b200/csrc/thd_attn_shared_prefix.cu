@@ -19,8 +19,10 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <numeric>
 #include <type_traits>
+#include <unordered_map>
 
 #include "../../include/thd_attn.h"
 #include "thd_sp_paged_kernel.cuh"
@@ -517,11 +519,49 @@ extern "C" int thd_attn_shared_prefix(const void* q, const void* k_cache, const 
     }
 }
 
+// Stalls found so far on a device, and how many of them each stream has been told of.
+// One word is enough for the kernels, but whoever reads it first must not take the
+// report away from the other streams, whose calls wrote nothing either.
+struct SpReports {
+    uint64_t stalls = 0;
+    int last = THD_OK;
+    std::unordered_map<void*, uint64_t> told;
+};
+static std::mutex g_sp_reports_mu;
+static SpReports g_sp_reports[64];
+
 extern "C" int thd_attn_shared_prefix_get_error(void* stream_ptr) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream_ptr)) != cudaSuccess) return THD_ERR_CUDA;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return THD_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_sp_reports_mu);
+    SpReports& r = g_sp_reports[dev];
     int s = 0;
     if (cudaMemcpyFromSymbol(&s, g_sp_status, sizeof(int)) != cudaSuccess) return THD_ERR_CUDA;
-    const int zero = 0;
-    if (s != 0 && cudaMemcpyToSymbol(g_sp_status, &zero, sizeof(int)) != cudaSuccess) return THD_ERR_CUDA;
-    return s;
+    if (s != 0) {
+        // The word stays until every call that it stops has ended: a merge that found it
+        // taken back would add up parts that were never written.
+        const int zero = 0;
+        if (cudaDeviceSynchronize() != cudaSuccess ||
+            cudaMemcpyToSymbol(g_sp_status, &zero, sizeof(int)) != cudaSuccess)
+            return THD_ERR_CUDA;
+        ++r.stalls;
+        r.last = s;
+    }
+    if (r.stalls == 0) return THD_OK;
+    try {
+        uint64_t& told = r.told[stream_ptr];
+        if (told == r.stalls) return THD_OK;
+        told = r.stalls;
+    } catch (...) {  // no host memory: the stream is told again next time
+    }
+    return r.last;
 }
+
+#if THD_DEBUG
+// Debug build: sets the status word, as a stalled kernel would (no kernel has to stall
+// for the tests of what follows a stall).
+extern "C" int thd_attn_shared_prefix_set_status(int status) {
+    return cudaMemcpyToSymbol(g_sp_status, &status, sizeof(int)) == cudaSuccess ? THD_OK : THD_ERR_CUDA;
+}
+#endif
