@@ -591,7 +591,7 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                     // Values of keys that no row of the group sees may be anything: zero
                     // them, as 0 * NaN would stay NaN.  (Whatever held V(j)'s slots before
                     // has been consumed by now, so their phase is this one's.)
-                    if (key0 < pc.lo || key0 + C::COLS > P) {
+                    if (key0 < pc.lo || key0 + C::COLS - 1 >= P) {  // (up to 2^31 - 1)
                         const int v_tiles = min(n, C::NSB + j) + j;  // K and V tiles before V(j)
 #pragma unroll 1
                         for (int s = 0; s < C::SUB && ok; ++s) {

@@ -203,3 +203,28 @@ def test_tables_in_place_replay_from_a_graph(B):
         check_outputs(got, want)
         seq, count, table, free = want["seq_lens"], want["free_count"], want["table"], want["free"]
         assert np.array_equal(tab.cpu().numpy(), table) and np.array_equal(fr.cpu().numpy(), free)
+
+
+# ------------------------------------------------ positions close to 2^31
+
+@pytest.mark.parametrize("rows", [8, 9])                  # the own pages' kernel takes the prefix; the prefix kernel does
+def test_prefix_of_nearly_two_to_the_31_keys(rows):
+    """A prefix table as long as the sizes allow, whose entries go through three
+    pages: keys and values are zero, so every weight is the same and the output
+    zero whatever the order of the sums; behind the last key there is NaN."""
+    block, D, n = 16, 64, 5
+    entries = 2 ** 27 - 2
+    P = entries * block - 5
+    assert (entries + 1) * block < 2 ** 31 and P + n < 2 ** 31
+    kc, vc = (torch.zeros((5, block, 1, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    for x in (kc, vc):
+        x[3, block - 5:] = float("nan")                   # the prefix's last page
+        x[4, n:] = float("nan")                           # the request's own
+    pt = torch.arange(entries, dtype=torch.int32, device=DEV).remainder_(3)
+    pt[-1] = 3
+    q = torch.ones((1, rows, D), dtype=torch.bfloat16, device=DEV)
+    out, lse = swa.thd_attn_shared_prefix(q, kc, vc, i32([[4]]), i32([n]), pt, torch.tensor([P], dtype=torch.int32, device=DEV))
+    assert swa.thd_attn_shared_prefix_get_error() == 0
+    assert (out == 0).all()
+    want = np.log(P + n)
+    assert np.abs(lse.cpu().numpy() - want).max() <= 2.0 ** -20 * (1 + want)
