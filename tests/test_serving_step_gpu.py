@@ -228,3 +228,37 @@ def test_prefix_of_nearly_two_to_the_31_keys(rows):
     assert (out == 0).all()
     want = np.log(P + n)
     assert np.abs(lse.cpu().numpy() - want).max() <= 2.0 ** -20 * (1 + want)
+
+
+# -------------------------- tables of every number of requests a thread takes
+
+def random_tables(B, block, M, seed):
+    rng = np.random.default_rng([seed, B])
+    seq, new = rng.integers(-1, M * block + 1, size=B), rng.integers(-1, 2 * block, size=B)
+    new[rng.uniform(size=B) < 0.2] = 0
+    held = np.where(seq > 0, -(-seq // block), 0)
+    pool = int(held.sum()) + B // 2                       # (pages run out)
+    perm = rng.permutation(pool).astype(np.int64)
+    table, at = np.full((B, M), -1), 0
+    for b in range(B):
+        table[b, :held[b]] = perm[at:at + held[b]]
+        at += held[b]
+    free = np.full(pool, -1)
+    free[:pool - at] = perm[at:]
+    rows = int(np.where((seq >= 0) & (new > 0), new, 0).sum()) + 3
+    return seq, new, table, free, pool - at, rows
+
+
+@pytest.mark.parametrize("B", [1024, 1025, 2047, 2048, 2049, 3001, 4095, 4096, 4097, 8191, 8192])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_tables_of_many_requests(B, in_place):
+    # one, two, four and eight requests a thread, the last thread's run cut or not
+    block, M = 8, 4
+    seq, new, table, free, count, rows = random_tables(B, block, M, 9)
+    want = OS.block_tables(seq, new, table, free, count, block, rows, 11)
+    assert 0 < want["refused"] < B
+    s, t, f, n = i32(seq), i32(table), i32(free), i32([count])
+    kw = dict(seq_lens_out=s, free_count_out=n) if in_place else {}
+    got = swa.thd_kv_block_tables(s, i32(new), t, f, n, block, rows, first_position=i32([11]), **kw)
+    check_outputs(got, want)
+    assert np.array_equal(t.cpu().numpy(), want["table"]) and np.array_equal(f.cpu().numpy(), want["free"])
