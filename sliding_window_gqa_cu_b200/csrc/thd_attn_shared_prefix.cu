@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(512) thd_sp_merge_kernel(const SpParams p, con
             u.cont_ml = p.pg_cont_ml + row;
         } else {
             const int row = rr % p.pg_rows;
-            count = p.pg_slice == 32 ? thd::sp_own_slices<32>(p, n) : thd::sp_own_slices<16>(p, n);
+            count = thd::sp_own_slices(p, n);
             u.home_rows = p.RB;
             u.cont_rows = p.pg_rows;
             u.home = p.own_home + bh * p.RB * D + rr * 4;
@@ -339,13 +339,12 @@ bool launch_prefix(const SpParams& p, const CUtensorMap& mk, const CUtensorMap& 
 }
 
 template <int D, int NR, int WR>
-bool launch_paged(SpParams& p, int* status, bool early, cudaStream_t stream) {
+bool launch_paged(const SpParams& p, int* status, bool early, cudaStream_t stream) {
     using C = thd::PagedConfig<D, NR, WR>;
-    p.pg_slice = C::KS;
     static std::atomic<uint64_t> done{0};
     return allow_smem(thd::thd_sp_paged_kernel<C>, C::SMEM_BYTES, done) &&
            launch_early(thd::thd_sp_paged_kernel<C>, dim3(p.pg_ctas), C::THREADS, C::SMEM_BYTES, stream, early,
-                        static_cast<const SpParams&>(p), status);
+                        p, status);
 }
 
 struct Maps {
@@ -358,6 +357,7 @@ int launch_all(SpParams p, const Maps& maps, cudaStream_t stream) {
     if (cudaGetSymbolAddress(&status, g_sp_status) != cudaSuccess) return THD_ERR_CUDA;
     int* st = static_cast<int*>(status);
     bool early = false;
+    p.pg_slice = p.pg_rows == 8 || D == 256 ? thd::PagedConfig<D, 1, 1>::KS : thd::PagedConfig<D, 2, 1>::KS;
     if (p.any_keys) {
         if (p.pre_lanes > 0) {
             if (!launch_prefix<D>(p, maps.k, maps.v, st, stream)) return THD_ERR_CUDA;

@@ -76,7 +76,7 @@ struct SpParams {
     int pg_units;       // row tiles of a request
     int pg_prefix;      // row tiles of the prefix that it takes (0: none)
     int pg_ctas;
-    int pg_slice;       // keys of a slice
+    int pg_slice;       // keys of a slice (16 or 32)
     float* own_home;
     float2* own_home_ml;
     long long* own_desc;  // first unit of an item
@@ -127,6 +127,23 @@ __device__ __forceinline__ int sp_own_slices(const SpParams& p, int n) {
     return n > 0 ? (n - 1) / KS + 1 - sp_first_own(p, n) / KS : 0;
 }
 
+__device__ __forceinline__ int sp_own_slices(const SpParams& p, int n) {
+    return p.pg_slice == 32 ? sp_own_slices<32>(p, n) : sp_own_slices<16>(p, n);
+}
+
+// What the paged kernel spends on a request of n own tokens, in keys of a kv head and
+// row tile that an SM reads meanwhile.  Starting and ending an item is latency that
+// other items hide once there is enough to read: an item of one key takes as long as
+// 64 keys of a long one, from some 100 keys on there is nothing to see of it.  Counting
+// keys alone gave the first tokens after a long prefix a few SMs, as if they cost
+// nothing: one token a request, 8 kv heads of 128, 64 requests after 4,096 tokens
+// 135 us against 37, 256 after 16,384 268 against 182.
+__device__ __forceinline__ float sp_own_cost(const SpParams& p, int n) {
+    if (n <= 0) return 0.0f;
+    const float sliced = static_cast<float>(sp_own_slices(p, n)) * p.pg_slice;
+    return fmaxf(static_cast<float>(n - sp_first_own(p, n)), 48.0f + 0.5f * sliced);
+}
+
 // Units of the prefix kernel for n_tiles key tiles.
 __device__ __forceinline__ long long sp_prefix_units(const SpParams& p, int n_tiles) {
     if (n_tiles <= 0) return 0;
@@ -142,21 +159,22 @@ struct SpSplit {
 // products and softmax, the paged kernel by memory, which half of the SMs can
 // keep busy, so both run side by side and the choice that ends the later one
 // soonest is taken.  The prefix takes kStart + tile * units / lanes; the requests'
-// own keys kStartPaged + bytes at an SM's rate each, kMemRate at most (ns, and bytes
-// a ns, as measured; row tiles of 32 and more are bound by their products, about
-// 0.57 TFLOP/s an SM, and read an item's keys once each).  Every thread has its own
-// candidates; the best of the warp wins.  64 requests on 8,191 tokens 92 us one
-// after the other, 75 side by side, 256 on 32,768 474 and 400; both kernels' CTAs on
+// own keys kStartPaged + their cost (sp_own_cost) at an SM's rate each, kMemRate at
+// most (ns, and bytes a ns, as measured; row tiles of 32 and more are bound by their
+// products, about 0.57 TFLOP/s an SM, and read an item's keys once each).  Every
+// thread has its own candidates; the best of the warp wins.  64 requests on 8,191
+// tokens 92 us one after the other, 75 side by side, 256 on 32,768 474 and 400 (both
+// before the power cap, under which the latter is 462); both kernels' CTAs on
 // the same SM 96 and 638 (the softmax warps lose more by waiting for issue slots and
 // loads than memory gains).  One rate for all row tiles: 64 requests of 16 rows,
 // 32,000 + 50..200 tokens, 272 against 165; one of 64 rows, 65,536 + 2,048, 446
 // against 96.
 template <int D>
-__device__ __forceinline__ SpSplit sp_split(const SpParams& p, long long units, float own_keys) {
+__device__ __forceinline__ SpSplit sp_split(const SpParams& p, long long units, float own_cost) {
     constexpr float kMemRate = 6000.0f, kStart = 10000.0f, kStartPaged = 12000.0f;
     constexpr float kSmRate = D == 64 ? 60.0f : 76.0f, kSmRate16 = D == 64 ? 55.0f : 50.0f, kSmRows = 570.0f;
     constexpr float kTile = D == 64 ? 1600.0f : 2300.0f;
-    const float bytes = own_keys * p.Hkv * p.pg_units * (D * 4);
+    const float bytes = own_cost * p.Hkv * p.pg_units * (D * 4);
     const float sm_rate = p.pg_rows <= 8 ? kSmRate : p.pg_rows <= 16 ? kSmRate16 : kSmRows / p.pg_rows;
     const int most = units > 0 ? sp_prefix_lanes(p, units) : 0;
     float best = INFINITY;

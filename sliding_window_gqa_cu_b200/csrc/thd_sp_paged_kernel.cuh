@@ -250,7 +250,7 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
             return n > 0 ? static_cast<long long>(sp_own_slices<C::KS>(p, n) + kItemUnits) * unit : 0;
         };
         int least = 0x7fffffff, longest = 0;  // own length; slices of an item
-        float keys = 0.0f;
+        float cost = 0.0f;
         long long mine = 0;
         for (int b = b0; b < b1; ++b) {
             const int n = sp_own_len(p, b);
@@ -258,7 +258,7 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
             if (n >= 0) least = min(least, n);
             if (n <= 0) continue;
             longest = max(longest, sp_own_slices<C::KS>(p, n));
-            keys += static_cast<float>(n - sp_first_own(p, n));
+            cost += sp_own_cost(p, n);
         }
         long long incl = mine;
 #pragma unroll
@@ -268,15 +268,15 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
         }
         least = __reduce_min_sync(0xffffffffu, least);
         longest = __reduce_max_sync(0xffffffffu, longest);
-        float* keys_of = reinterpret_cast<float*>(smem);
+        float* cost_of = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
+        for (int o = 16; o > 0; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
         if (lane == 31) start[warp] = incl;
-        if (lane == 0) keys_of[warp] = keys;
+        if (lane == 0) cost_of[warp] = cost;
         if (lane == 0) start[4 + warp] = static_cast<long long>(longest) << 32 | least;
         __syncthreads();
         long long before = incl - mine, total = 0;
-        keys = keys_of[0] + keys_of[1] + keys_of[2] + keys_of[3];
+        cost = cost_of[0] + cost_of[1] + cost_of[2] + cost_of[3];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             if (w < warp) before += start[w];
@@ -301,7 +301,7 @@ thd_sp_paged_kernel(const SpParams p, int* status) {
         // One wave of CTAs on the SMs that the prefix kernel leaves.
         int ctas = p.pg_ctas;
         if (p.pre_lanes > 0 && lo < P)
-            ctas = min(ctas, C::RESIDENT * max(1, sp_split<C::D>(p, sp_prefix_units(p, (P - 1) / 128 + 1 - lo / 128), keys).free));
+            ctas = min(ctas, C::RESIDENT * max(1, sp_split<C::D>(p, sp_prefix_units(p, (P - 1) / 128 + 1 - lo / 128), cost).free));
         const int lanes = static_cast<int>(min((units + least_units - 1) / least_units,
                                                static_cast<long long>(ctas) * C::WORKERS));
         // Where each worker's range begins among the own units.

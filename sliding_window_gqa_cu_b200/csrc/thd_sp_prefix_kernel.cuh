@@ -65,7 +65,7 @@ struct PrefixConfig {
 
     static constexpr int SMEM_SLOTS = NT * Q_TILE_BYTES;
     static constexpr int SMEM_BAR = SMEM_SLOTS + NSLOT * SLOT_BYTES;
-    static constexpr int SMEM_MIN = SMEM_BAR + NUM_BARS * 8;  // [2][16]: least own length, own keys of a warp's requests
+    static constexpr int SMEM_MIN = SMEM_BAR + NUM_BARS * 8;  // [2][16]: least own length, cost of the own keys of a warp's requests
     static constexpr int SMEM_XCH = SMEM_MIN + 32 * 4;          // float [NSB][NT][2][128]: maxima (sums) of two threads of a row
     static constexpr int SMEM_TMEM_SLOT = SMEM_XCH + (HALVES > 1 ? NSB * NT * 2 * 128 * 4 : 0);
     static constexpr int SMEM_ABORT = SMEM_TMEM_SLOT + 4;
@@ -148,7 +148,7 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::SMEM_ABORT);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SMEM_TMEM_SLOT);
     int* warp_min = reinterpret_cast<int*>(smem + C::SMEM_MIN);
-    float* warp_keys = reinterpret_cast<float*>(warp_min + 16);
+    float* warp_cost = reinterpret_cast<float*>(warp_min + 16);
 
     if (threadIdx.x == 0) {
         for (int q = 0; q < C::NT; ++q) {
@@ -176,33 +176,33 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         tma_prefetch_desc(&tmap_k);
         tma_prefetch_desc(&tmap_v);
     }
-    // Least own length (for the first key that any row sees) and all own keys.
+    // Least own length (for the first key that any row sees) and what all own keys cost.
     const int P = sp_prefix_len(p);
     {
         int n = 0x7fffffff;
-        float keys = 0.0f;
+        float cost = 0.0f;
         for (int b = threadIdx.x; b < p.n_req; b += C::THREADS) {
             const int len = sp_own_len(p, b);
             if (len < 0) continue;
             n = min(n, len);
-            keys += static_cast<float>(len - sp_first_own(p, len));
+            cost += sp_own_cost(p, len);
         }
         n = __reduce_min_sync(0xffffffffu, n);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
+        for (int o = 16; o > 0; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
         if (lane == 0) {
             warp_min[warp] = n;
-            warp_keys[warp] = keys;
+            warp_cost[warp] = cost;
         }
     }
     __syncthreads();
     PrefixWalk<C> walk;
     {
         int n = 0x7fffffff;
-        float keys = 0.0f;
+        float cost = 0.0f;
         for (int w = 0; w < C::THREADS / 32; ++w) {
             n = min(n, warp_min[w]);
-            keys += warp_keys[w];
+            cost += warp_cost[w];
         }
         const int lo = n == 0x7fffffff ? P : sp_first_key(p, P + n - p.n_q);
         walk.first_tile = lo / C::BN;
@@ -211,7 +211,7 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         walk.member = blockIdx.x % p.pre_width;
         const int my_lane = blockIdx.x / p.pre_width;
         const long long units = sp_prefix_units(p, walk.n_tiles);
-        const int lanes = sp_split<C::D>(p, units, keys).lanes;
+        const int lanes = sp_split<C::D>(p, units, cost).lanes;
         walk.x = lanes > 0 ? lane_begin(units, lanes, my_lane) : 0;
         walk.x1 = lanes > 0 ? lane_begin(units, lanes, my_lane + 1) : 0;
         if (blockIdx.x == 0 && threadIdx.x == 0) {
