@@ -21,7 +21,7 @@ SOURCES = [os.path.join(CSRC, "thd_attn_api.cu"), os.path.join(CSRC, "thd_attn_n
            os.path.join(CSRC, "scheduler.cpp")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("thd_attn_kernel.cuh", "thd_attn_split_kernel.cuh",
                                                   "thd_attn_bwd_kernels.cuh", "thd_sp_common.cuh", "sp_lanes.h",
-                                                  "thd_sp_prefix_kernel.cuh", "thd_sp_paged_kernel.cuh",
+                                                  "sp_ring.h", "thd_sp_prefix_kernel.cuh", "thd_sp_paged_kernel.cuh",
                                                   "sm100_ptx.cuh", "scheduler.h", "tma_map.h")] \
     + [os.path.join(ROOT, "include", "thd_attn.h")]
 

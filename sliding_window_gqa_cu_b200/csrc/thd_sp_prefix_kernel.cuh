@@ -23,6 +23,7 @@
 // the matrix descriptors need it.
 #pragma once
 
+#include "sp_ring.h"
 #include "thd_attn_kernel.cuh"
 #include "thd_sp_common.cuh"
 
@@ -252,34 +253,27 @@ thd_sp_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                 if (pc.n == 0) continue;
                 int next = place_of(pc.kt, pc.h);
                 int j = 0;  // this warp's next tile
-                // The slots of one tile of K or V, in order of consumption.  Both warps
-                // wait for every slot, so that neither can be a phase ahead.
-                auto tile = [&](bool v) {
+                ok = ring_piece<C::NSB>(pc.n, [&](bool v) {
                     const bool load = v == is_v;
+                    if (!load) mine <<= C::SUB;
                     const int place = next;
                     if (load && j + 1 < pc.n) next = place_of(pc.kt + j + 1, pc.h);
                     const int eight = (((pc.kt + j) * C::BN + box * p.box_rows) & (p.block - 1)) >> 3;
-                    for (int s = 0; s < C::SUB && ok; ++s) {
-                        const int slot = pos % C::NSLOT;
-                        ok = warp_wait(bar(C::B_SLOT_EMPTY + slot), ((pos / C::NSLOT) & 1) ^ 1, abort_flag, status);
-                        if (!ok) return;
-                        if (load) {
+                    if (load) ++j;
+                    return ring_tile(
+                        load, C::SUB, C::NSLOT, pos,
+                        [&](int slot, int parity) {
+                            return warp_wait(bar(C::B_SLOT_EMPTY + slot), parity, abort_flag, status);
+                        },
+                        [&](int s, int slot) {
                             if (lane == 0) mbar_arrive_expect_tx(bar(C::B_SLOT_FULL + slot), C::SLOT_BYTES);
                             __syncwarp();
                             if (lane < boxes)
                                 tma_load_5d(sbase + C::SMEM_SLOTS + slot * C::SLOT_BYTES + box * (p.box_rows / 8) * C::GROUP_BYTES,
                                             map, bar(C::B_SLOT_FULL + slot), 0, 0, s * C::CH, eight, place);
-                        }
-                        mine = mine << 1 | (load ? 1u : 0u);
-                        ++pos;
-                    }
-                    if (load) ++j;
-                };
-                for (int i = 0; i < C::NSB && i < pc.n; ++i) tile(false);
-                for (int i = 0; i < pc.n && ok; ++i) {
-                    tile(true);
-                    if (i + C::NSB < pc.n && ok) tile(false);
-                }
+                            mine = mine << 1 | 1u;
+                        });
+                });
             }
             if (!ok && lane == 0)  // let the loads in flight land before the CTA ends
                 for (int i = 0; i < C::NSLOT && i < pos; ++i)

@@ -291,3 +291,24 @@ def test_few_own_tokens_cost_no_more_than_many(B, P):
     # reading 200 tokens a request is more work than reading one; the SMs were shared as
     # if items without keys to speak of took no time (135 against 43 us for 64 requests)
     assert call_us(B, 1, P) <= 1.3 * call_us(B, 200, P)
+
+
+# --------------------------------------------------------- many calls in a row
+
+@pytest.mark.parametrize("D,B,Hq,Hkv,P,own", [(256, 64, 16, 1, 32768, 700), (128, 64, 64, 8, 16384, 700), (64, 128, 32, 8, 32768, 700)])
+def test_many_calls_without_a_stall_and_with_the_same_bits(D, B, Hq, Hkv, P, own):
+    # both producers of the prefix's ring, with pages all over the cache and memory busy
+    block = 16
+    per, pages = -(-own // block), P // block
+    g = torch.Generator(device=DEV).manual_seed(7)
+    kc, vc, q = (torch.randn(s, generator=g, device=DEV).to(torch.bfloat16) for s in
+                 ((pages + B * per, block, Hkv, D), (pages + B * per, block, Hkv, D), (B, Hq, D)))
+    perm = torch.randperm(pages + B * per, generator=g, device=DEV).to(torch.int32)
+    args = (q, kc, vc, perm[pages:].view(B, per).contiguous(), i32([own] * B), perm[:pages].contiguous(), i32([P]))
+    ws = torch.empty((swa.thd_attn_shared_prefix_workspace_bytes(B, 1, Hq, Hkv, D),), dtype=torch.uint8, device=DEV)
+    first = swa.thd_attn_shared_prefix(*args, workspace=ws)
+    for i in range(3000):
+        out = swa.thd_attn_shared_prefix(*args, workspace=ws)
+        if i % 300 == 299:
+            assert swa.thd_attn_shared_prefix_get_error() == 0
+            assert torch.equal(out[0], first[0]) and torch.equal(out[1], first[1])
