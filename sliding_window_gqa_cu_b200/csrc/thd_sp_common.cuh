@@ -168,11 +168,16 @@ struct SpSplit {
 // the same SM 96 and 638 (the softmax warps lose more by waiting for issue slots and
 // loads than memory gains).  One rate for all row tiles: 64 requests of 16 rows,
 // 32,000 + 50..200 tokens, 272 against 165; one of 64 rows, 65,536 + 2,048, 446
-// against 96.
+// against 96.  With few SMs for the own pages they read, at D = 64, 128 and 256, 61 to
+// 66, 73 to 92 and 59 to 77 bytes a ns each (8 rows), 54, 38 to 42 and 31 to 37 (16
+// rows); a tile takes 1,850, 2,130 and 1,800 to 2,100 ns.  44 at D = 256 is between that
+// and 50, where requests of 200 tokens got too few SMs (256 on 65,536: 490 us, with 44
+// 268); 36 would be as fast there and costs the prefix with a window 2 us in 56.
 template <int D>
 __device__ __forceinline__ SpSplit sp_split(const SpParams& p, long long units, float own_cost) {
     constexpr float kMemRate = 6000.0f, kStart = 10000.0f, kStartPaged = 12000.0f;
-    constexpr float kSmRate = D == 64 ? 60.0f : 76.0f, kSmRate16 = D == 64 ? 55.0f : 50.0f, kSmRows = 570.0f;
+    constexpr float kSmRate = D == 64 ? 60.0f : 76.0f, kSmRows = 570.0f;
+    constexpr float kSmRate16 = D == 64 ? 55.0f : D == 128 ? 50.0f : 44.0f;
     constexpr float kTile = D == 64 ? 1600.0f : 2300.0f;
     const float bytes = own_cost * p.Hkv * p.pg_units * (D * 4);
     const float sm_rate = p.pg_rows <= 8 ? kSmRate : p.pg_rows <= 16 ? kSmRate16 : kSmRows / p.pg_rows;

@@ -293,6 +293,11 @@ def test_few_own_tokens_cost_no_more_than_many(B, P):
     assert call_us(B, 1, P) <= 1.3 * call_us(B, 200, P)
 
 
+def test_fewer_own_tokens_cost_no_more_at_head_dim_256():
+    kw = dict(P=65536, Hq=16, Hkv=1, D=256)
+    assert call_us(256, 200, **kw) <= 1.1 * call_us(256, 1000, **kw)      # (490 against 410 us with too high a rate)
+
+
 # --------------------------------------------------------- many calls in a row
 
 @pytest.mark.parametrize("D,B,Hq,Hkv,P,own", [(256, 64, 16, 1, 32768, 700), (128, 64, 64, 8, 16384, 700), (64, 128, 32, 8, 32768, 700)])
