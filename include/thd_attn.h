@@ -541,10 +541,14 @@ int thd_kv_write(const void* k, const void* v, int64_t k_row_stride, int64_t v_r
  * THD_ERR_UNSUPPORTED.  (prefix_blocks + max_blocks) * block_size < 2^31,
  * window >= 0, scale finite and > 0; out of range THD_ERR_INVALID_ARG.
  * n_req = 0 is a no-op.  Kernel stalls are reported by
- * thd_attn_shared_prefix_get_error.  (num_blocks - 1) * block_stride +
- * (Hkv - 1) * head_stride, in units of the greatest common divisor of the two
- * strides, has to stay below 2^31 (any pool of whole pages does), else
- * THD_ERR_UNSUPPORTED.
+ * thd_attn_shared_prefix_get_error.  With a prefix and more than 32 rows
+ * (n_req * n_q * Hq / Hkv), (num_blocks - 1) * block_stride + (Hkv - 1) *
+ * head_stride, in units of the greatest common divisor of the two strides, has
+ * to stay below 2^31 (any pool of whole pages does), else THD_ERR_UNSUPPORTED.
+ * n_q is the same for all requests of a call.  A request with fewer new tokens
+ * may take part with rows in front: they count as queries of the positions
+ * before (so the keys that they see have to be finite too), and their out and
+ * lse mean nothing to the caller.  Or it goes into a call of its own.
  * Up to three launches, the later ones begun early on the same stream
  * (programmatic dependent launch): what follows on the stream waits for all.
  * thd_attn_shared_prefix_workspace_bytes returns 0 for sizes that are not

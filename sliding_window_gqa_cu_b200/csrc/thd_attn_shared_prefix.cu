@@ -217,13 +217,20 @@ constexpr int kPagedCtas = 3 * thd::kSpLanes;  // three fit an SM
 constexpr int kAnyPlacesRows = 32;
 
 // Whether the paged kernel takes a prefix (of at most `tokens`, what its table
-// holds) too, once per row tile: it is done with few keys before another launch
-// has started.  Same rows and heads (8 of 128), paged against prefix kernel, us:
-// 16 rows 8,191 keys 32 and 36, 65,536 keys 116 and 84; 32 rows 37 and 38, 173 and
-// 103; 64 rows 1,000 keys 22 and 27, 8,191 keys 44 and 38.  Tiles of more rows are
-// bound by products and those of 256 columns have slower slices: 16 rows of a
-// request, 4,000 keys 34 and 32.  One tile of 8 rows leaves the prefix kernel
-// nothing to share (65,536 keys 75 and 84).
+// holds: the length itself lies on the device) too, once per row tile: it is done with
+// few keys before another launch has started.  Paged against prefix kernel, whole
+// calls with 100 own tokens, us:
+//   8 kv heads of 128  16 rows 4,096 keys 26 and 27, 8,192 32 and 32; 32 rows 4,096 27 and
+//                      28, 8,192 37 and 33; 64 rows 1,024 22 and 26, 4,096 32 and 29; 256 rows
+//                      1,024 30 and 29
+//   8 kv heads of 64   the same to within 5 %
+//   2 kv heads of 128  fewer SMs share the work of a long prefix: 8 rows 4,096 keys 9 %
+//                      slower, 16,384 15 %; 64 rows 4,096 keys 6 % faster, 256 rows
+//                      1,024 14 %
+// so 2^18 rows times keys is within 20 % either way of where the two meet.  Tiles of more
+// rows are bound by products and those of 256 columns have slower slices (8 rows of 256
+// columns: 2,048 keys 7 to 11 % slower, 4,096 30 %).  One tile of 8 rows leaves the prefix
+// kernel little to share (8 kv heads of 128: 5 to 18 % faster up to 32,768 keys).
 bool prefix_by_pages(int tiles, int tile_rows, int64_t tokens, int D) {
     if (tile_rows == 8 && D <= 128) return tiles == 1 || tokens * tiles * tile_rows <= 1 << 18;
     return tokens <= 2048 && tokens * tiles * tile_rows <= 1 << 18;

@@ -6,12 +6,15 @@
 // rows as the 8 columns: S^T = K Q^T and O^T = V^T P^T, so that 8 query rows (a
 // group of 8 heads) leave no lane of the product idle, Q^T, the scores and O^T
 // stay in registers, and 32 keys of head dim 128 take some 250 instructions per
-// warp while their 16 KB take longer to arrive.  (A tcgen05 tile would be 128 rows
-// high, 1/16 of it used, and send the scores through TMEM.)
+// warp while their 16 KB take longer to arrive.  With 8 query rows a tcgen05 tile
+// would send the scores through TMEM for products that are not what bounds this; from
+// 32 rows on, with the keys as its 128 rows and the query rows as its columns, it would
+// be full, and these tiles are bound by mma.sync (below): not built.
 //
 // P goes into its product as a bf16 number and a second one for what that rounding
-// lost (2^-17 is left): the products are not what bounds the kernel, and a single
-// rounding would add as much error as that of the output.
+// lost (2^-17 is left): up to 16 rows the products are not what bounds the kernel, and a
+// single rounding would add as much error as that of the output.  Row tiles of 32 and 64
+// pay for it (three products a slice instead of two) and keep it for that error's sake.
 //
 // A worker is WR warps of 8 NR rows each, which share a ring of slots (a K or V
 // slice of KS keys each) and refill a slot as soon as it has been read.  Workers

@@ -42,7 +42,7 @@ int run(int nslot, int sub, int consumers, unsigned seed, int late) {
         const auto t0 = Clock::now();
         while (!b.done(parity)) {
             if (bad) return false;
-            if (Clock::now() - t0 > std::chrono::milliseconds(1500)) { bad = 1; return false; }
+            if (Clock::now() - t0 > std::chrono::seconds(20)) { bad = 1; return false; }
             std::this_thread::yield();
         }
         return true;
