@@ -819,13 +819,14 @@ def thd_attn_shared_prefix_workspace_bytes(n_req: int, n_q: int, Hq: int, Hkv: i
 
 def thd_attn_shared_prefix_get_error(stream=None) -> int:
     """Synchronise the stream and return the last stall of
-    :func:`thd_attn_shared_prefix` on the current device that this stream has not
-    been told of (0: none).  After a stall the calls of all streams write nothing
+    :func:`thd_attn_shared_prefix` on the stream's device that it has not been told
+    of (0: none).  After a stall the calls of all streams write nothing
     until one asks; every stream is told, once."""
     import torch
     if stream is None:
         stream = torch.cuda.current_stream()
-    return int(load_library().thd_attn_shared_prefix_get_error(ctypes.c_void_p(stream.cuda_stream)))
+    with torch.cuda.device(stream.device):
+        return int(load_library().thd_attn_shared_prefix_get_error(ctypes.c_void_p(stream.cuda_stream)))
 
 
 def thd_attn_selftest_stall() -> tuple:

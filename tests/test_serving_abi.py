@@ -124,3 +124,30 @@ def test_workspace_of_unsupported_sizes(lib):
     assert f(4097, 1, 8, 2, 128) == 0 and f(1 << 20, 1 << 20, 8, 2, 128) == 0 and f(2, 1, 258, 2, 128) == 0
     assert f(2, 1, 8, 2, 96) == 0 and f(2, 1, 7, 2, 128) == 0
     assert f(4096, 1, 8, 8, 64) > 0 and f(1, 4096 * 128, 8, 8, 64) > 0
+
+
+def test_status_is_read_on_the_streams_device(monkeypatch):
+    # a stream of the second device, the first one current: that device's word
+    class Library:
+        def thd_attn_shared_prefix_get_error(self, handle):
+            seen.append((current[-1], handle.value))
+            return -4
+
+    class Device:
+        def __init__(self, device):
+            self.index = torch.device(device).index
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0x1234
+
+    seen, current = [], [0]
+    monkeypatch.setattr(swa, "load_library", Library)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    assert swa.thd_attn_shared_prefix_get_error(Stream()) == -4
+    assert seen == [(1, 0x1234)] and current == [0]
